@@ -301,6 +301,105 @@ pk_status pk_resolve(int64_t n, int64_t cand_budget, float collision_ratio, int3
 pk_status pk_select_candidates_noalloc(const uint8_t *S, int64_t n, int64_t C, int32_t *cand,
                                        void *stream);
 
+/* ---------------------------------------------------------------------------
+ * A KV cache held in 4 bits, attended whole, and eviction from it by
+ * accumulated attention weight.  (No counterpart on the pages: a second way to
+ * keep a long context on the GPU, beside retrieval -- a quarter of the bf16
+ * rows' bytes, every key attended, and a bounded number of keys.)
+ *
+ * The cache belongs to the caller: pk_quant_cache only describes its buffers,
+ * the calls allocate nothing, keep nothing between calls and may be recorded
+ * into a CUDA graph.  Each pair bh = b * n_kv_heads + h has its own length
+ * lens[bh], read on the GPU by every call, so sequences may be ragged (or
+ * empty) and a replayed graph sees the current lengths.
+ *   blocks  [bh][n_cap / 32][4608] bytes, 16-byte aligned.  A block of 32 keys:
+ *             [32][64] B  K codes      [32][64] B  V codes
+ *             [32][4]     K scales     [32][4]     V scales      (bf16, >= 0)
+ *           A row's 128 channels are four groups of 32 channels; a value is
+ *           (code - 8) * scale of its group.  Nibble p of a row is half p & 1
+ *           (0: low) of byte p >> 1:
+ *             K  nibble 32 t + 8 r + i  is channel 32 r + 8 t + i   (r, t < 4, i < 8)
+ *             V  nibble 16 c + 4 r + i  is channel 32 r + 8 i + g   (r, i < 4, g < 8),
+ *                c = g, or g ^ 4 in the keys j of a block with (j & 2) != 0
+ *           (the orders in which the matrix instructions of pk_quant_attend
+ *           take them).
+ *   lens    [bh] i32: keys of each pair, 0 <= lens <= n_cap.
+ *   acc     [bh][n_cap] f32 or NULL: accumulated attention weight of each key.
+ *   status  [2] i32 or NULL: the device-check word of the calls on this cache.
+ *           The first failed check writes {PK_ERR_DEVICE_CHECK, pair}; the
+ *           caller clears it.  A length outside 0..n_cap is such a check; it
+ *           is read as the nearest bound.
+ * Rows at or behind a pair's length are never read as keys: they may hold any
+ * bytes.  The calls leave them as they are.
+ * Two calls on one cache must not overlap on the GPU if one of them writes it
+ * (append and eviction write it; attention writes acc only when it
+ * accumulates). */
+enum { PK_QUANT_KEYS = 32, PK_QUANT_BLOCK_BYTES = 4608 };
+typedef struct {
+    int32_t bh;               /* pairs, 1 <= bh <= 65535                        */
+    int32_t kv_dtype;         /* pk_dtype of the rows and queries of the calls  */
+    int64_t n_cap;            /* keys per pair, a multiple of 32                */
+    void *blocks;
+    int32_t *lens;
+    float *acc;
+    int32_t *status;
+} pk_quant_cache;
+
+/* Quantise rows into the cache: row i of pair bh goes to slot at[bh] + i, and
+ * lens[bh] becomes at[bh] + n_new.  Per group of 32 channels
+ *   scale = bf16(fp32(max |x| / 7)),  code = 8 + clamp(round(x / scale), -7, 7),
+ * rounded to the nearest integer, ties to even (|x - value| <= scale / 2 up to
+ * the scale's own rounding; zeros stay zero).  A group that holds an infinity
+ * or a NaN gets the scale NaN: all its values read back as NaN.
+ *   k_new, v_new  [bh][src_stride][D] kv_dtype; rows 0..n_new-1 are taken.
+ *                 src_stride 0 means n_new.
+ *   at            [bh] i32 device, or NULL: lens itself (append at the end).
+ * With acc, the weights of the new slots start at zero.  A pair whose rows do
+ * not fit (at < 0 or at + n_new > n_cap) is left as it is, lens included, and
+ * the device check records it. */
+pk_status pk_quant_append(const pk_quant_cache *cache, const void *k_new, const void *v_new, int64_t n_new,
+                          int64_t src_stride, const int32_t *at, void *stream);
+
+/* Read rows back as values: slot at[bh] + i of pair bh (at NULL: slot i) to row
+ * i of k_out, v_out [bh][n_rows][D] kv_dtype (bf16: rounded to nearest even).
+ * Rows of slots outside 0..lens[bh]-1 are left as they are. */
+pk_status pk_quant_rows(const pk_quant_cache *cache, int64_t n_rows, void *k_out, void *v_out, const int32_t *at,
+                        void *stream);
+
+/* Bytes of workspace that pk_quant_attend needs on the current device for
+ * this cache (any lengths up to n_cap).  It needs no initialisation; two calls
+ * that share a workspace must not overlap on the GPU. */
+pk_status pk_quant_attend_workspace(const pk_quant_cache *cache, int32_t group, int32_t accumulate, size_t *bytes);
+
+/* Exact softmax attention of every query head over all keys of its pair.
+ *   q      [bh][group][D] kv_dtype (= [batch][H*G][D]: query head j of a
+ *          sequence belongs to KV head j/G); 1 <= group <= 8.
+ *   scale  softmax scale; 0 = 1/sqrt(D).
+ *   out    [bh][group][D] f32: sum_j p_j V_j, p = softmax_j(scale <q, K_j>);
+ *          zeros for a pair without keys.
+ *   lse    [bh][group] f32 or NULL: log sum_j exp(scale <q, K_j>) (-inf without
+ *          keys): what merging with attention over other rows needs.
+ *   accumulate  non-zero: acc[bh][j] += sum over the pair's query heads of p_j
+ *          (the cache must have acc).
+ *   work   work_bytes bytes, 256-byte aligned device memory.
+ * PK_ERR_CAPACITY when work_bytes is too small. */
+pk_status pk_quant_attend(const pk_quant_cache *cache, const void *q, int32_t group, float scale, float *out,
+                          float *lse, int32_t accumulate, void *work, size_t work_bytes, void *stream);
+
+/* Evict by accumulated weight: of every pair of src keep the first `sink`
+ * keys, the last `recent` keys, and of the keys between them those of the
+ * largest acc (ties: the lower slot; NaN counts as the smallest), `budget` in
+ * all; a pair of at most `budget` keys keeps all.  The kept rows, weights (if
+ * dst has acc) and lengths go to dst, in their order, from slot 0 on; src is
+ * not changed.
+ *   src, dst  same bh and kv_dtype, buffers that do not overlap; src has acc;
+ *             dst->n_cap >= min(budget, src->n_cap).
+ *   budget    >= 1; sink, recent >= 0; sink + recent <= budget.
+ *   keep      [bh][budget] i32 or NULL: the kept slots of src, ascending; -1
+ *             behind a pair's last. */
+pk_status pk_quant_evict(const pk_quant_cache *src, const pk_quant_cache *dst, int64_t budget, int64_t sink,
+                         int64_t recent, int32_t *keep, void *stream);
+
 /* Per-kernel timing.  While tracing is on, the library records a CUDA event
  * pair on the launching stream around each of its kernels.  pk_trace_read
  * synchronises, then returns per kernel kind (0 encode, 1 query_prep,

@@ -12,8 +12,8 @@ import ctypes as C
 import numpy as np
 
 from . import _lib
-from ._lib import (KERNELS, PK_BF16, PK_F32, PK_KV_DEVICE, PK_KV_HOST_PINNED, PK_OK, pk_debug_out,
-                   pk_info, pk_params)
+from ._lib import (KERNELS, PK_BF16, PK_F32, PK_KV_DEVICE, PK_KV_HOST_PINNED, PK_OK, PK_QUANT_BLOCK_BYTES,
+                   PK_QUANT_KEYS, pk_debug_out, pk_info, pk_params, pk_quant_cache)
 
 _handle = None
 
@@ -40,6 +40,8 @@ __all__ = [
     "pk_select_candidates_noalloc", "pk_attend_dense", "pk_search_heads", "pk_attend_heads",
     "pk_append_stage", "pk_append_publish", "pk_params", "pk_info", "pk_debug_out", "PK_F32",
     "PK_BF16", "PK_KV_DEVICE", "PK_KV_HOST_PINNED", "KERNELS", "lib",
+    "pk_quant_cache", "pk_quant_view", "pk_quant_append", "pk_quant_rows", "pk_quant_attend_workspace",
+    "pk_quant_attend", "pk_quant_evict", "PK_QUANT_KEYS", "PK_QUANT_BLOCK_BYTES",
 ]
 
 
@@ -202,3 +204,58 @@ def pk_select_candidates_noalloc(S, n: int, C: int, cand, stream=None):
     include/pariskv.h): for callers that cannot allocate at that moment."""
     _check(_L().pk_select_candidates_noalloc(_ptr(S), int(n), int(C), _ptr(cand), _stream(stream)),
            "pk_select_candidates_noalloc")
+
+
+def pk_quant_view(blocks, lens, kv_dtype: int, acc=None, status=None) -> pk_quant_cache:
+    """Descriptor of a 4-bit KV cache in the caller's tensors: blocks
+    [bh][n_cap / 32][4608] u8, lens [bh] i32, acc [bh][n_cap] f32, status [2]
+    i32, dense (format in include/pariskv.h).  It keeps the tensors alive."""
+    import torch
+    if blocks.dim() != 3 or blocks.shape[2] != PK_QUANT_BLOCK_BYTES:
+        raise ValueError("blocks must be [bh][n_cap / %d][%d] bytes" % (PK_QUANT_KEYS, PK_QUANT_BLOCK_BYTES))
+    bh, n_cap = blocks.shape[0], blocks.shape[1] * PK_QUANT_KEYS
+    for name, t, shape, dtype in (("blocks", blocks, tuple(blocks.shape), torch.uint8), ("lens", lens, (bh,), torch.int32),
+                                  ("acc", acc, (bh, n_cap), torch.float32), ("status", status, (2,), torch.int32)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError("%s must be a dense %s tensor of shape %s" % (name, dtype, shape))
+    c = pk_quant_cache(bh, int(kv_dtype), n_cap, _ptr(blocks), _ptr(lens), _ptr(acc), _ptr(status))
+    c.tensors = (blocks, lens, acc, status)
+    return c
+
+
+def pk_quant_append(cache, k_new, v_new, n_new: int, at=None, src_stride: int = 0, stream=None):
+    """Quantise rows 0..n_new-1 per pair of k_new/v_new [bh][src_stride][D] into
+    slots at[bh].. (None: the end of the pair); lens becomes at + n_new."""
+    _check(_L().pk_quant_append(cache, _ptr(k_new), _ptr(v_new), int(n_new), int(src_stride), _ptr(at),
+                                _stream(stream)), "pk_quant_append")
+
+
+def pk_quant_rows(cache, n_rows: int, k_out, v_out, at=None, stream=None):
+    """Read slots at[bh].. (None: 0..) back as values into k_out/v_out [bh][n_rows][D]."""
+    _check(_L().pk_quant_rows(cache, int(n_rows), _ptr(k_out), _ptr(v_out), _ptr(at), _stream(stream)),
+           "pk_quant_rows")
+
+
+def pk_quant_attend_workspace(cache, group: int, accumulate: bool = False) -> int:
+    """Bytes of workspace for pk_quant_attend on this cache."""
+    n = C.c_size_t(0)
+    _check(_L().pk_quant_attend_workspace(cache, int(group), 1 if accumulate else 0, C.byref(n)),
+           "pk_quant_attend_workspace")
+    return n.value
+
+
+def pk_quant_attend(cache, q, group: int, out, work, lse=None, accumulate: bool = False, scale: float = 0.0,
+                    stream=None):
+    """Attention of q [bh][group][D] over every key of its pair into out (f32)
+    and lse; accumulate adds the keys' weights to the cache's acc.  work: a
+    tensor of pk_quant_attend_workspace bytes."""
+    _check(_L().pk_quant_attend(cache, _ptr(q), int(group), float(scale), _ptr(out), _ptr(lse),
+                                1 if accumulate else 0, _ptr(work), work.numel() * work.element_size(),
+                                _stream(stream)), "pk_quant_attend")
+
+
+def pk_quant_evict(src, dst, budget: int, sink: int = 0, recent: int = 0, keep=None, stream=None):
+    """Keep the first `sink`, the last `recent` and the heaviest other keys of
+    every pair of src, `budget` in all, in dst; keep [bh][budget] gets their slots."""
+    _check(_L().pk_quant_evict(src, dst, int(budget), int(sink), int(recent), _ptr(keep), _stream(stream)),
+           "pk_quant_evict")

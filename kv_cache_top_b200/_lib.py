@@ -17,12 +17,14 @@ EXPORTS = (
     "pk_export_index", "pk_magnitude_levels", "pk_resolve", "pk_trace_enable", "pk_trace_read",
     "pk_select_candidates_noalloc", "pk_attend_dense", "pk_search_heads", "pk_attend_heads",
     "pk_append_stage", "pk_append_publish",
+    "pk_quant_append", "pk_quant_rows", "pk_quant_attend_workspace", "pk_quant_attend", "pk_quant_evict",
 )
 
 PK_OK, PK_ERR_INVALID_ARG, PK_ERR_CAPACITY, PK_ERR_OOM, PK_ERR_CUDA, PK_ERR_TIMEOUT, \
     PK_ERR_DEVICE_CHECK, PK_ERR_UNSUPPORTED = range(8)
 PK_F32, PK_BF16 = 0, 1
 PK_KV_DEVICE, PK_KV_HOST_PINNED = 0, 1
+PK_QUANT_KEYS, PK_QUANT_BLOCK_BYTES = 32, 4608
 KERNELS = ("encode", "query_prep", "collision_scan", "compact", "rerank_topk", "topk_merge",
            "gather_attend")
 
@@ -50,6 +52,13 @@ class pk_debug_out(C.Structure):
     _fields_ = [
         ("qt", C.c_void_p), ("qnorm", C.c_void_p), ("bonus", C.c_void_p), ("S", C.c_void_p),
         ("hist", C.c_void_p), ("sstar", C.c_void_p), ("cand", C.c_void_p), ("cand_est", C.c_void_p),
+    ]
+
+
+class pk_quant_cache(C.Structure):
+    _fields_ = [
+        ("bh", C.c_int32), ("kv_dtype", C.c_int32), ("n_cap", C.c_int64), ("blocks", C.c_void_p),
+        ("lens", C.c_void_p), ("acc", C.c_void_p), ("status", C.c_void_p),
     ]
 
 
@@ -103,4 +112,15 @@ def load() -> C.CDLL:
     lib.pk_trace_read.argtypes = [P, P, P]
     lib.pk_select_candidates_noalloc.restype = st
     lib.pk_select_candidates_noalloc.argtypes = [P, I64, I64, P, P]
+    QC = C.POINTER(pk_quant_cache)
+    lib.pk_quant_append.restype = st
+    lib.pk_quant_append.argtypes = [QC, P, P, I64, I64, P, P]
+    lib.pk_quant_rows.restype = st
+    lib.pk_quant_rows.argtypes = [QC, I64, P, P, P, P]
+    lib.pk_quant_attend_workspace.restype = st
+    lib.pk_quant_attend_workspace.argtypes = [QC, I32, I32, C.POINTER(C.c_size_t)]
+    lib.pk_quant_attend.restype = st
+    lib.pk_quant_attend.argtypes = [QC, P, I32, F32, P, P, I32, P, C.c_size_t, P]
+    lib.pk_quant_evict.restype = st
+    lib.pk_quant_evict.argtypes = [QC, QC, I64, I64, I64, P, P]
     return lib

@@ -1,0 +1,554 @@
+"""The 4-bit KV cache (pk_quant_*): rows in and out, attention over the cache,
+eviction by accumulated weight, each against a plain 64-bit implementation of
+the documented format (tests/quant_ref.py)."""
+import ctypes as C
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import quant_ref as ref
+
+gpu = pytest.mark.gpu
+D, KEYS, BLOCK = 128, 32, 4608
+
+
+@pytest.fixture(scope="module")
+def pk():
+    from kv_cache_top_b200 import build
+    build.build()
+    import kv_cache_top_b200 as pk
+    return pk
+
+
+def dt(pk, name):
+    return (torch.bfloat16, pk.PK_BF16) if name == "bf16" else (torch.float32, pk.PK_F32)
+
+
+def make_rows(rng, n, dtype, scale=1.0):
+    spread = np.exp(0.5 * rng.standard_normal(D))
+    return torch.from_numpy((rng.standard_normal((n, D)) * spread * scale).astype(np.float32)).to(dtype)
+
+
+def make_cache(pk, rng, lens, cap, kind, acc=None, status=True, v_scale=1.0):
+    """A cache on the GPU of the given lengths; rows behind a length are 0xff bytes."""
+    bh = len(lens)
+    blocks = np.full((bh, cap // KEYS, BLOCK), 0xff, np.uint8)
+    dtype = torch.bfloat16 if kind == pk.PK_BF16 else torch.float32
+    for p, n in enumerate(lens):
+        if n:
+            b = ref.pack(make_rows(rng, n, dtype).float().numpy(), make_rows(rng, n, dtype, v_scale).float().numpy())
+            blocks[p, :len(b)] = b
+    t = torch.from_numpy(blocks).cuda()
+    st = torch.zeros(2, dtype=torch.int32, device="cuda") if status else None
+    a = None if acc is None else torch.from_numpy(acc.astype(np.float32)).cuda()
+    return pk.pk_quant_view(t, torch.tensor(lens, dtype=torch.int32, device="cuda"), kind, acc=a, status=st), blocks
+
+
+# ---------------------------------------------------------------- on the CPU
+def test_reference_format_round_trip():
+    """The test's packing and decoding agree with each other and with the documented bound."""
+    rng = np.random.default_rng(0)
+    K, V = (make_rows(rng, 45, torch.float32).numpy() for _ in range(2))
+    b = ref.pack(K, V)
+    k, v = ref.values(b)
+    for x, y in ((K, k), (V, v)):
+        assert np.array_equal(y[:45], ref.stored(x)[2])
+        s = ref.stored(x)[1][:, ref.GROUP]
+        assert np.all(np.abs(x - y[:45]) <= s * (0.5 + 7 * 2.0 ** -8))     # half a step, and the scale's rounding
+    assert sorted(ref.K_NIB) == list(range(D)) and all(sorted(v) == list(range(D)) for v in ref.V_NIB)
+
+
+def test_refusals_before_any_launch(pk):
+    lib, L = pk.lib, pk._lib
+    fake = 1 << 20                       # never dereferenced: sizes are checked first, then the pointers
+    one = C.c_size_t()
+
+    def view(bh=2, kind=1, cap=64, blocks=fake, lens=fake, acc=None, status=None):
+        return pk.pk_quant_cache(bh, kind, cap, blocks, lens, acc, status)
+
+    size = lambda c, g=4, a=0: lib.pk_quant_attend_workspace(c, g, a, C.byref(one))  # noqa: E731
+    assert size(view()) == L.PK_OK and one.value > 0 and one.value % 256 == 0
+    small = one.value
+    assert size(view(), 4, 1) == L.PK_OK and one.value == small + 2 * 4 * 64 * 4
+    assert size(None) == L.PK_ERR_INVALID_ARG
+    for bad in (view(bh=0), view(kind=2), view(cap=0), view(cap=33), view(cap=-32)):
+        assert size(bad) == L.PK_ERR_INVALID_ARG
+    assert size(view(bh=65536)) == L.PK_ERR_UNSUPPORTED
+    assert size(view(cap=1 << 31)) == L.PK_ERR_CAPACITY
+    assert size(view(), 0) == L.PK_ERR_INVALID_ARG and size(view(), 9) == L.PK_ERR_INVALID_ARG
+    assert lib.pk_quant_attend_workspace(view(), 4, 0, None) == L.PK_ERR_INVALID_ARG
+    # without a GPU no pointer is device memory: every launching call refuses
+    assert lib.pk_quant_append(None, None, None, 1, 0, None, None) == L.PK_ERR_INVALID_ARG
+    assert lib.pk_quant_append(view(blocks=None), fake, fake, 1, 0, None, None) == L.PK_ERR_INVALID_ARG
+    assert lib.pk_quant_rows(view(lens=None), 1, fake, fake, None, None) == L.PK_ERR_INVALID_ARG
+    assert lib.pk_quant_attend(view(), None, 4, 0.0, None, None, 0, None, 0, None) == L.PK_ERR_INVALID_ARG
+    assert lib.pk_quant_evict(view(), None, 1, 0, 0, None, None) == L.PK_ERR_INVALID_ARG
+
+
+def test_view_checks_tensors(pk):
+    blocks, lens = torch.zeros(2, 3, BLOCK, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    c = pk.pk_quant_view(blocks, lens, pk.PK_BF16)
+    assert (c.bh, c.n_cap, c.kv_dtype) == (2, 96, pk.PK_BF16) and c.blocks == blocks.data_ptr() and not c.acc
+    for bad in (dict(blocks=blocks[:, :, :100]), dict(blocks=blocks.to(torch.int8)), dict(lens=lens.long()),
+                dict(lens=torch.zeros(3, dtype=torch.int32)), dict(acc=torch.zeros(2, 64)),
+                dict(acc=torch.zeros(2, 96, dtype=torch.float64)), dict(status=torch.zeros(1, dtype=torch.int32)),
+                dict(blocks=torch.zeros(2, 6, BLOCK, dtype=torch.uint8)[:, ::2])):
+        with pytest.raises(ValueError):
+            pk.pk_quant_view(**{**dict(blocks=blocks, lens=lens, kv_dtype=pk.PK_BF16), **bad})
+
+
+# ---------------------------------------------------------------- refusals with real pointers
+@gpu
+def test_gpu_refusals(pk):
+    rng = np.random.default_rng(1)
+    c, _ = make_cache(pk, rng, [3, 40], 64, pk.PK_BF16, acc=np.zeros((2, 64)))
+    plain, _ = make_cache(pk, rng, [3, 40], 64, pk.PK_BF16)
+    k = torch.zeros(2, 4, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(2, 4, D, device="cuda")
+    work = torch.empty(pk.pk_quant_attend_workspace(c, 4, True), dtype=torch.uint8, device="cuda")
+
+    def refused(status, f, *args, **kw):
+        with pytest.raises(pk.PkError) as e:
+            f(*args, **kw)
+        assert e.value.status == status, (f, e.value.status)
+
+    bad, cap = pk._lib.PK_ERR_INVALID_ARG, pk._lib.PK_ERR_CAPACITY
+    refused(bad, pk.pk_quant_append, c, k, k, 0)
+    refused(cap, pk.pk_quant_append, c, k, k, 65)
+    refused(bad, pk.pk_quant_append, c, k, k, 4, src_stride=3)
+    refused(bad, pk.pk_quant_append, c, k.cpu(), k, 4)
+    refused(bad, pk.pk_quant_append, c, k.data_ptr() + 1, k, 4)
+    refused(bad, pk.pk_quant_append, c, k, k, 4, at=torch.zeros(2, dtype=torch.int32))
+    refused(bad, pk.pk_quant_rows, c, 0, k, k)
+    refused(bad, pk.pk_quant_rows, c, 1, None, k)
+    refused(bad, pk.pk_quant_attend, c, k, 0, out, work)
+    refused(bad, pk.pk_quant_attend, c, k, 9, out, work)
+    refused(bad, pk.pk_quant_attend, c, k, 4, out, work, scale=-1.0)
+    refused(bad, pk.pk_quant_attend, c, k, 4, out, work, scale=math.nan)
+    refused(bad, pk.pk_quant_attend, c, k, 4, out, work, scale=math.inf)
+    refused(bad, pk.pk_quant_attend, c, k, 4, out.data_ptr() + 2, work)
+    refused(bad, pk.pk_quant_attend, plain, k, 4, out, work, accumulate=True)
+    refused(bad, pk.pk_quant_attend, c, k, 4, out, work[8:])
+    refused(cap, pk.pk_quant_attend, c, k, 4, out, work[:-256], accumulate=True)
+    d, _ = make_cache(pk, rng, [0, 0], 32, pk.PK_BF16, acc=np.zeros((2, 32)))
+    refused(bad, pk.pk_quant_evict, plain, d, 32)                    # no weights to go by
+    refused(bad, pk.pk_quant_evict, c, d, 0)
+    refused(bad, pk.pk_quant_evict, c, d, 32, sink=-1)
+    refused(bad, pk.pk_quant_evict, c, d, 32, sink=20, recent=13)
+    refused(cap, pk.pk_quant_evict, c, d, 33)
+    refused(bad, pk.pk_quant_evict, c, c, 32)
+    f32, _ = make_cache(pk, rng, [0, 0], 64, pk.PK_F32)
+    refused(bad, pk.pk_quant_evict, c, f32, 32)
+    few, _ = make_cache(pk, rng, [0], 64, pk.PK_BF16)
+    refused(bad, pk.pk_quant_evict, c, few, 32)
+    torch.cuda.synchronize()
+    assert c.tensors[1].tolist() == [3, 40] and c.tensors[3].tolist() == [0, 0]
+
+
+# ---------------------------------------------------------------- rows in and out
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,n_new,stride,shift", [
+    ([0], 1, 0, 0), ([31], 1, 0, 0), ([0, 5, 63], 1, 3, 1), ([0, 1, 30, 33], 64, 0, 0), ([7, 0], 65, 70, 1),
+    ([2, 100], 333, 0, 2), ([0] * 5, 32, 0, 8),
+])
+def test_append_codes_are_exact(pk, dtype, lens, n_new, stride, shift):
+    """Codes and scales of every new row are the reference's; other bytes of the cache do not change; lengths grow.
+    `shift` elements off the 16-byte boundary."""
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(len(lens) * 1000 + n_new)
+    cap = -(-(max(lens) + n_new) // KEYS) * KEYS + KEYS
+    bh, st = len(lens), stride or n_new
+    c, before = make_cache(pk, rng, lens, cap, kind, acc=rng.random((bh, cap)))
+    acc0 = c.tensors[2].cpu().numpy()
+    rows = []
+    for _ in range(2):
+        x = make_rows(rng, bh * st, td)
+        x[::3, 5] *= 9
+        x[1::4, 32:64] = 0
+        x[::5, 96:] = x[::5, 96:].sign() * torch.tensor(rng.integers(0, 8, 32), dtype=td) * 0.5    # ties and borders
+        flat = torch.zeros(x.numel() + shift, dtype=td, device="cuda")
+        flat[shift:] = x.flatten().cuda()
+        rows.append((x.view(bh, st, D), flat[shift:].view(bh, st, D)))
+    pk.pk_quant_append(c, rows[0][1], rows[1][1], n_new, src_stride=stride)
+    got = c.tensors[0].cpu().numpy()
+    assert c.tensors[1].tolist() == [n + n_new for n in lens] and c.tensors[3].tolist() == [0, 0]
+    for p, n in enumerate(lens):
+        kc, vc, ks, vs = ref.decode(got[p])
+        for code, s, x in ((kc, ks, rows[0][0]), (vc, vs, rows[1][0])):
+            want, scale, _ = ref.stored(x[p, :n_new].float().numpy())
+            assert np.array_equal(s[n:n + n_new], scale)
+            assert np.array_equal(code[n:n + n_new], want)
+        for a, b in zip(ref.decode(before[p]), (kc, vc, ks, vs)):
+            keep = np.ones(cap, bool)
+            keep[n:n + n_new] = False
+            assert np.array_equal(a[keep], b[keep], equal_nan=True)
+        acc = c.tensors[2][p].cpu().numpy()
+        assert np.all(acc[n:n + n_new] == 0) and np.array_equal(acc[:n], acc0[p, :n]) and \
+            np.array_equal(acc[n + n_new:], acc0[p, n + n_new:])
+
+
+@gpu
+def test_append_extreme_values(pk):
+    """Subnormal, huge, infinite and NaN values; a group's neighbours are not touched by it."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((12, D)).astype(np.float32)
+    x[0] *= np.float32(1e-44)
+    x[1] *= np.float32(1e-40)
+    x[2] *= np.float32(1e-38)
+    x[3] *= np.float32(2e37)
+    x[4, 3], x[5, 40], x[6, 127] = np.inf, -np.inf, np.nan
+    x[7] = 0
+    x[8] = -0.0
+    x[9, :] = 0
+    x[9, 64] = np.float32(1e-45)
+    x[10, :32] = np.float32(3.0e38) * np.sign(x[10, :32])
+    x[11] *= np.float32(1e-19)
+    c, _ = make_cache(pk, rng, [0], 32, pk.PK_F32)
+    t = torch.from_numpy(x).cuda()[None].contiguous()
+    pk.pk_quant_append(c, t, t.flip(1).contiguous(), 12)
+    kc, vc, ks, vs = ref.decode(c.tensors[0][0].cpu().numpy())
+    k, v = torch.empty_like(t), torch.empty_like(t)
+    pk.pk_quant_rows(c, 12, k, v)
+    for code, s, y, back in ((kc, ks, x, k), (vc, vs, x[::-1], v)):
+        want, scale, val = ref.stored(y)
+        assert np.array_equal(s[:12], scale, equal_nan=True)
+        live = np.repeat(scale > 0, 32, 1)
+        assert np.array_equal(code[:12][live], want[live])
+        with np.errstate(over="ignore", invalid="ignore"):
+            assert np.array_equal(back[0].cpu().numpy(), val.astype(np.float32), equal_nan=True)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_at_places_and_refuses_what_does_not_fit(pk, dtype):
+    td, kind = dt(pk, dtype)
+    for n_new in (3, 70):                # one CTA per pair, several
+        rng = np.random.default_rng(n_new)
+        cap = 128
+        lens = [50, 60, 70, 80, 90]
+        c, before = make_cache(pk, rng, lens, cap, kind)
+        at = torch.tensor([10, cap - n_new, cap - n_new + 1, -1, 0], dtype=torch.int32, device="cuda")
+        x = make_rows(rng, 5 * n_new, td).view(5, n_new, D).cuda()
+        pk.pk_quant_append(c, x, x, n_new, at=at)
+        got = c.tensors[0].cpu().numpy()
+        assert c.tensors[1].tolist() == [10 + n_new, cap, 70, 80, n_new]
+        assert c.tensors[3][0].item() == pk._lib.PK_ERR_DEVICE_CHECK and c.tensors[3][1].item() in (2, 3)
+        for p in (2, 3):
+            assert np.array_equal(got[p], before[p])
+        for p, a in ((0, 10), (1, cap - n_new), (4, 0)):
+            k, v = ref.values(got[p])
+            val = ref.stored(x[p].float().cpu().numpy())[2]
+            assert np.array_equal(k[a:a + n_new], val) and np.array_equal(v[a:a + n_new], val)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_rows_values_and_untouched_rows(pk, dtype, shift):
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(9)
+    lens, n_rows = [0, 1, 33, 200], 100
+    c, blocks = make_cache(pk, rng, lens, 224, kind)
+    at = torch.tensor([0, 0, -5, 150], dtype=torch.int32, device="cuda")
+    k = torch.full((4 * n_rows * D + shift,), 7.0, dtype=td, device="cuda")[shift:].view(4, n_rows, D)
+    v = torch.full((4 * n_rows * D + shift,), 7.0, dtype=td, device="cuda")[shift:].view(4, n_rows, D)
+    for a, use in ((at, at.tolist()), (None, [0] * 4)):
+        k.fill_(7.0)
+        v.fill_(7.0)
+        pk.pk_quant_rows(c, n_rows, k, v, at=a)
+        for p, n in enumerate(lens):
+            kv = ref.values(blocks[p])
+            for got, val in zip((k, v), kv):
+                for i in range(n_rows):
+                    slot = use[p] + i
+                    want = torch.from_numpy(val[slot].astype(np.float32)).to(td) if 0 <= slot < n else torch.full((D,), 7.0, dtype=td)
+                    assert torch.equal(got[p, i].cpu(), want), (p, i)
+
+
+# ---------------------------------------------------------------- attention
+def check_attend(pk, c, blocks, lens, q, G, scale=None, accumulate=False, acc0=None, calls=1):
+    bh = len(lens)
+    out = torch.full((bh, G, D), 5.0, device="cuda")
+    lse = torch.full((bh, G), 5.0, device="cuda")
+    work = torch.full((pk.pk_quant_attend_workspace(c, G, accumulate),), 0xff, dtype=torch.uint8, device="cuda")
+    for _ in range(calls):
+        pk.pk_quant_attend(c, q, G, out, work, lse=lse, accumulate=accumulate, scale=scale or 0.0)
+    out, lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    for p, n in enumerate(lens):
+        K, V = ref.values(blocks[p])
+        o, l, w, eo, el, ew = ref.attend(q[p].double().cpu().numpy(), K[:n], V[:n], scale)
+        assert np.all(np.abs(out[p] - o) <= eo), (p, n, np.max(np.abs(out[p] - o) / eo))
+        if n:
+            assert np.all(np.abs(lse[p] - l) <= el), (p, n, np.max(np.abs(lse[p] - l) / el))
+        else:
+            assert np.all(lse[p] == -np.inf)
+        if accumulate:
+            got = c.tensors[2][p].cpu().double().numpy()
+            want = acc0[p].copy()
+            want[:n] += calls * w.sum(0)
+            # a rounding of the sum per call and head, and each weight's own error
+            tol = calls * ((w * ew[:, None]).sum(0) + (G + 1) * ref.U * np.abs(want[:n])) + 1e-37
+            assert np.all(np.abs(got[:n] - want[:n]) <= tol), (p, n, np.max(np.abs(got[:n] - want[:n]) / tol))
+            assert np.array_equal(got[n:], acc0[p][n:])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8])
+def test_attend_lengths_from_none_to_many(pk, dtype, G):
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(G)
+    lens = [0, 1, 2, 31, 32, 33, 63, 64, 65, 0, 100, 1000, 1024, 0]
+    acc0 = rng.random((len(lens), 1024)).astype(np.float32)
+    c, blocks = make_cache(pk, rng, lens, 1024, kind, acc=acc0)
+    q = make_rows(rng, len(lens) * G, td).view(len(lens), G, D).cuda()
+    check_attend(pk, c, blocks, lens, q, G)
+    check_attend(pk, c, blocks, lens, q, G, accumulate=True, acc0=acc0.astype(np.float64), calls=2)
+    assert c.tensors[3].tolist() == [0, 0]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,G,lens", [
+    ("bf16", 4, [20011]), ("f32", 1, [4096]), ("f32", 8, [9001, 1, 0, 5000]), ("bf16", 8, [8192, 8191]),
+    ("bf16", 1, [0]), ("f32", 3, [0, 0, 0]), ("bf16", 4, [577] * 300), ("f32", 2, [1] * 1500 + [40] * 3),
+])
+def test_attend_splits(pk, dtype, G, lens):
+    """Long pairs over many workers, many pairs in one worker, nothing at all."""
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(len(lens) + G)
+    cap = max(32, -(-max(lens) // KEYS) * KEYS)
+    acc0 = np.zeros((len(lens), cap), np.float32)
+    c, blocks = make_cache(pk, rng, lens, cap, kind, acc=acc0)
+    q = (1.5 * make_rows(rng, len(lens) * G, td)).to(td).view(len(lens), G, D).cuda()
+    check_attend(pk, c, blocks, lens, q, G, accumulate=True, acc0=acc0.astype(np.float64))
+    check_attend(pk, c, blocks, lens, q, G, scale=0.011)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_q_off_the_boundary(pk, dtype):
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(12)
+    c, blocks = make_cache(pk, rng, [70, 10], 96, kind)
+    flat = torch.zeros(2 * 4 * D + 1, dtype=td, device="cuda")
+    flat[1:] = make_rows(rng, 8, td).flatten().cuda()
+    check_attend(pk, c, blocks, [70, 10], flat[1:].view(2, 4, D), 4)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qs,vs", [(1e-3, 1.0), (40.0, 1.0), (1.0, 1e-25), (1.0, 1e25), (1e-30, 1e-10), (0.0, 1.0)])
+def test_attend_magnitudes(pk, dtype, qs, vs):
+    """Flat and one-hot softmax, tiny and huge values and queries."""
+    td, kind = dt(pk, dtype)
+    rng = np.random.default_rng(77)
+    lens = [500, 33]
+    acc0 = np.zeros((2, 512), np.float32)
+    c, blocks = make_cache(pk, rng, lens, 512, kind, acc=acc0, v_scale=vs)
+    q = (qs * make_rows(rng, 8, torch.float32)).to(td).view(2, 4, D).cuda()
+    check_attend(pk, c, blocks, lens, q, 4, accumulate=True, acc0=acc0.astype(np.float64))
+
+
+@gpu
+def test_attend_values_of_mixed_size(pk):
+    """Keys whose values are 2^40 or 2^-40 of their neighbours', zero rows, and a key of huge values that no query
+    looks at: each contributes what its weight says."""
+    rng = np.random.default_rng(8)
+    n = 300
+    K, V = make_rows(rng, n, torch.float32).numpy(), make_rows(rng, n, torch.float32).numpy()
+    q = make_rows(rng, 4, torch.float32).numpy()
+    V[::7] *= np.float32(2.0 ** -40)
+    V[5] *= np.float32(2.0 ** 40)
+    V[::11] = 0
+    K[77] = -50 * q[0]                   # weight about e^-400 for head 0
+    V[77] = 1e30
+    K[78] = 0
+    blocks = np.full((1, 10, BLOCK), 0xff, np.uint8)
+    b = ref.pack(K, V)
+    blocks[0, :len(b)] = b
+    for kind, td in ((pk.PK_F32, torch.float32), (pk.PK_BF16, torch.bfloat16)):
+        c = pk.pk_quant_view(torch.from_numpy(blocks).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), kind)
+        qq = torch.from_numpy(np.repeat(q[:1], 4, 0)).to(td).cuda()[None].contiguous()
+        check_attend(pk, c, blocks, [n], qq, 4)
+
+
+@gpu
+def test_attend_nan_stays_in_its_group_of_values(pk):
+    """A NaN group of V makes its 32 channels NaN and no others; a NaN group of K makes all of the pair NaN; rows
+    behind the length (0xff bytes) and other pairs do not matter."""
+    rng = np.random.default_rng(6)
+    c, blocks = make_cache(pk, rng, [50, 50, 50], 64, pk.PK_F32, status=False)
+    blocks[0, 0, 4352 + 8 * 9 + 2 * 1:][:2] = 0xff       # V scale of key 9, group 1
+    blocks[1, 1, 4096 + 8 * 3 + 2 * 2:][:2] = 0xff       # K scale of key 35, group 2
+    c.tensors[0].copy_(torch.from_numpy(blocks))
+    q = make_rows(rng, 6, torch.float32).view(3, 2, D).cuda()
+    out = torch.zeros(3, 2, D, device="cuda")
+    pk.pk_quant_attend(c, q, 2, out, torch.empty(pk.pk_quant_attend_workspace(c, 2), dtype=torch.uint8, device="cuda"))
+    out = out.cpu().double().numpy()
+    K, V = ref.values(blocks[0])
+    live = np.r_[0:32, 64:128]
+    o, _, _, eo, _, _ = ref.attend(q[0].double().cpu().numpy(), K[:50], np.where(np.isnan(V[:50]), 0, V[:50]))
+    assert np.isnan(out[0][:, 32:64]).all() and np.all(np.abs(out[0] - o)[:, live] <= eo[:, live])
+    assert np.isnan(out[1]).all()
+    K, V = ref.values(blocks[2])
+    o, _, _, eo, _, _ = ref.attend(q[2].double().cpu().numpy(), K[:50], V[:50])
+    assert np.all(np.abs(out[2] - o) <= eo)
+
+
+@gpu
+def test_attend_bad_lengths_are_clamped_and_recorded(pk):
+    rng = np.random.default_rng(4)
+    c, blocks = make_cache(pk, rng, [64, 64, 20], 64, pk.PK_BF16)
+    c.tensors[1].copy_(torch.tensor([64, 65, -3], dtype=torch.int32))
+    q = make_rows(rng, 3, torch.bfloat16).view(3, 1, D).cuda()
+    check_attend(pk, c, blocks, [64, 64, 0], q, 1)
+    assert c.tensors[3][0].item() == pk._lib.PK_ERR_DEVICE_CHECK and c.tensors[3][1].item() in (1, 2)
+
+
+# ---------------------------------------------------------------- eviction
+def check_evict(pk, src, blocks, lens, acc, dst_cap, kind, budget, sink, recent, with_acc=True, with_keep=True):
+    bh = len(lens)
+    fill = np.full((bh, dst_cap // KEYS, BLOCK), 0xA5, np.uint8)
+    dst = pk.pk_quant_view(torch.from_numpy(fill).cuda(), torch.full((bh,), -9, dtype=torch.int32, device="cuda"), kind,
+                           acc=torch.full((bh, dst_cap), 3.0, device="cuda") if with_acc else None)
+    keep = torch.full((bh, budget), -7, dtype=torch.int32, device="cuda") if with_keep else None
+    pk.pk_quant_evict(src, dst, budget, sink=sink, recent=recent, keep=keep)
+    got = dst.tensors[0].cpu().numpy()
+    assert np.array_equal(src.tensors[0].cpu().numpy(), blocks)
+    for p, n in enumerate(lens):
+        want = ref.evict(acc[p], n, budget, sink, recent)
+        m = len(want)
+        assert dst.tensors[1][p].item() == m
+        if with_keep:
+            assert np.array_equal(keep[p].cpu().numpy(), np.concatenate([want, np.full(budget - m, -1)]))
+        if with_acc:
+            assert np.array_equal(dst.tensors[2][p, :m].cpu().numpy(), acc[p][want], equal_nan=True)
+            assert np.all(dst.tensors[2][p, m:].cpu().numpy() == 3.0)
+        a, b, old = ref.decode(blocks[p]), ref.decode(got[p]), ref.decode(fill[p])
+        for x, y, z in zip(a, b, old):
+            assert np.array_equal(x[want], y[:m], equal_nan=True), (p, n)
+            assert np.array_equal(y[m:], z[m:], equal_nan=True)
+
+
+@gpu
+@pytest.mark.parametrize("lens,budget,sink,recent", [
+    ([0, 1, 2, 5], 1, 0, 0), ([0, 1, 2, 5], 1, 1, 0), ([7, 3, 64], 3, 1, 1), ([100, 90, 10], 40, 4, 36),
+    ([100, 1000, 1023, 1024], 100, 3, 17), ([2000, 333, 999], 999, 64, 512), ([4096, 4095], 4094, 0, 0),
+    ([5000] * 3, 32, 0, 32), ([3001, 20000], 1500, 64, 256),
+])
+@pytest.mark.parametrize("weights", ["heavy", "ties", "odd"])
+def test_evict_keeps_the_heaviest(pk, lens, budget, sink, recent, weights):
+    rng = np.random.default_rng(budget + len(lens))
+    cap = -(-max(lens) // KEYS) * KEYS + 32
+    bh = len(lens)
+    if weights == "heavy":
+        acc = np.exp(2 * rng.standard_normal((bh, cap)) - 5)
+    elif weights == "ties":
+        acc = rng.integers(0, 3, (bh, cap)) * 0.25
+    else:                                # both zeros, negatives, infinities, NaN: an order all the same
+        acc = rng.choice([0.0, -0.0, -1.0, np.inf, -np.inf, np.nan, 1e-45, -1e-45, 2.5], (bh, cap))
+    acc = acc.astype(np.float32)
+    src, blocks = make_cache(pk, rng, lens, cap, pk.PK_BF16, acc=acc)
+    dst_cap = -(-min(budget, cap) // KEYS) * KEYS
+    check_evict(pk, src, blocks, lens, acc, dst_cap, pk.PK_BF16, budget, sink, recent)
+    check_evict(pk, src, blocks, lens, acc, dst_cap + 64, pk.PK_BF16, budget, sink, recent, with_acc=False, with_keep=False)
+
+
+@gpu
+def test_evict_long_rows(pk):
+    """Longer than anything held on chip at once, the threshold's ties over the whole row."""
+    rng = np.random.default_rng(3)
+    n, cap = 300001, 300032
+    blocks = torch.randint(0, 255, (2, cap // KEYS, BLOCK), dtype=torch.uint8, device="cuda")
+    acc = np.exp(rng.standard_normal((2, cap))).astype(np.float32)
+    acc[1] = rng.integers(0, 4, cap)
+    src = pk.pk_quant_view(blocks, torch.tensor([n, n - 7], dtype=torch.int32, device="cuda"), pk.PK_F32,
+                           acc=torch.from_numpy(acc).cuda())
+    for budget in (1000, 200000):
+        check_evict(pk, src, blocks.cpu().numpy(), [n, n - 7], acc, -(-budget // KEYS) * KEYS, pk.PK_F32, budget, 10, 300)
+
+
+# ---------------------------------------------------------------- together
+@gpu
+def test_calls_in_a_captured_graph_on_another_stream(pk):
+    """append + attend + evict recorded once and replayed: the replay sees the lengths and rows of its time."""
+    rng = np.random.default_rng(21)
+    bh, G, cap = 3, 4, 128
+    lens = [5, 0, 64]
+    acc0 = np.zeros((bh, cap), np.float32)
+    c, _ = make_cache(pk, rng, lens, cap, pk.PK_BF16, acc=acc0)
+    e = pk.pk_quant_view(torch.zeros(bh, 1, BLOCK, dtype=torch.uint8, device="cuda"),
+                         torch.zeros(bh, dtype=torch.int32, device="cuda"), pk.PK_BF16, acc=torch.zeros(bh, 32, device="cuda"))
+    k, v = (torch.zeros(bh, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(bh, G, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros(bh, G, D, device="cuda"), torch.zeros(bh, G, device="cuda")
+    work = torch.empty(pk.pk_quant_attend_workspace(c, G, True), dtype=torch.uint8, device="cuda")
+    keep = torch.zeros(bh, 32, dtype=torch.int32, device="cuda")
+
+    def step():
+        pk.pk_quant_append(c, k, v, 1)
+        pk.pk_quant_attend(c, q, G, out, work, lse=lse, accumulate=True)
+        pk.pk_quant_evict(c, e, 32, sink=1, recent=4, keep=keep)
+
+    start = [t.clone() for t in c.tensors[:3]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                           # warm up off the capture
+        for t, s in zip(c.tensors, start):
+            t.copy_(s)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    acc = acc0.astype(np.float64)
+    for it in range(40):
+        new = [make_rows(rng, bh, torch.bfloat16).view(bh, 1, D) for _ in range(2)]
+        k.copy_(new[0])
+        v.copy_(new[1])
+        q.copy_(make_rows(rng, bh * G, torch.bfloat16).view(bh, G, D))
+        graph.replay()
+        blocks, o = c.tensors[0].cpu().numpy(), out.cpu().double().numpy()
+        for p, n0 in enumerate(lens):
+            n = n0 + it + 1
+            assert c.tensors[1][p].item() == n
+            K, V = ref.values(blocks[p])
+            assert np.array_equal(K[n - 1], ref.stored(new[0][p].float().numpy())[2][0])
+            assert np.array_equal(V[n - 1], ref.stored(new[1][p].float().numpy())[2][0])
+            want, _, w, eo, _, _ = ref.attend(q[p].double().cpu().numpy(), K[:n], V[:n])
+            assert np.all(np.abs(o[p] - want) <= eo)
+            acc[p, :n] += w.sum(0)
+            mine = c.tensors[2][p].cpu().numpy()
+            assert np.allclose(mine[:n], acc[p, :n], rtol=1e-3, atol=1e-6)
+            kept = ref.evict(mine, n, 32, 1, 4)
+            assert np.array_equal(keep[p].cpu().numpy()[:len(kept)], kept) and e.tensors[1][p].item() == len(kept)
+            ek, ev = ref.values(e.tensors[0][p].cpu().numpy())
+            assert np.array_equal(ek[:len(kept)], K[kept]) and np.array_equal(ev[:len(kept)], V[kept])
+
+
+@gpu
+def test_two_streams_with_their_own_workspaces(pk):
+    """Two calls at once over one cache that neither writes."""
+    rng = np.random.default_rng(30)
+    lens, G = [4000, 300, 17], 4
+    c, blocks = make_cache(pk, rng, lens, 4000, pk.PK_F32)
+    res, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s in streams:
+        q = make_rows(rng, 3 * G, torch.float32).view(3, G, D).cuda()
+        out = torch.zeros(3, G, D, device="cuda")
+        work = torch.empty(pk.pk_quant_attend_workspace(c, G), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        res.append((q, out, work))
+    for _ in range(5):
+        for s, (q, out, work) in zip(streams, res):
+            pk.pk_quant_attend(c, q, G, out, work, stream=s)
+    torch.cuda.synchronize()
+    for q, out, _ in res:
+        for p, n in enumerate(lens):
+            K, V = ref.values(blocks[p])
+            o, _, _, eo, _, _ = ref.attend(q[p].double().cpu().numpy(), K[:n], V[:n])
+            assert np.all(np.abs(out[p].cpu().double().numpy() - o) <= eo)
