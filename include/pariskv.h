@@ -307,8 +307,8 @@ pk_status pk_select_candidates_noalloc(const uint8_t *S, int64_t n, int64_t C, i
  * keep a long context on the GPU, beside retrieval -- a quarter of the bf16
  * rows' bytes, every key attended, and a bounded number of keys.)
  *
- * The cache belongs to the caller: pk_quant_cache only describes its buffers,
- * the calls allocate nothing, keep nothing between calls and may be recorded
+ * The cache belongs to the caller: pk_quant_cache only describes its buffers
+ * (device memory of the current device); the calls allocate nothing, keep nothing between calls and may be recorded
  * into a CUDA graph.  Each pair bh = b * n_kv_heads + h has its own length
  * lens[bh], read on the GPU by every call, so sequences may be ragged (or
  * empty) and a replayed graph sees the current lengths.

@@ -4,28 +4,45 @@
 // softmax per worker's segment of a pair and a merge of the segments; when
 // weights are accumulated, the logits go to the workspace and the merge
 // kernel, which knows each head's log-sum, adds the weights to acc.
+#include <cuda_fp16.h>
+
 #include "pk_launch.cuh"
 #include "pk_quant.cuh"
 
 namespace pk {
 
-constexpr int kQaThreads = 128;
-constexpr int kQaMinShare = 8;           // blocks a worker takes at least
+constexpr int kQaWarps = 12;
+constexpr int kQaThreads = 32 * kQaWarps;
+constexpr int kQaStages = 3;             // blocks in flight per warp
+constexpr int kQaMinShare = kQaWarps;    // blocks a worker takes at least: one per warp
+constexpr int kQaCol = kD + 4;           // floats between the columns of a warp's sums in shared memory
 constexpr int kQmThreads = 256;          // merge kernel
 constexpr int kQmKeys = 2048;            // keys of a merge CTA's part of acc
 
-int quant_attend_workers(int num_sms) { return min(4 * num_sms, kQMaxWorkers); }
+struct QaSmem {
+    uint8_t ring[kQaWarps][kQaStages][kQBlock];
+    unsigned long long bar[kQaWarps][kQaStages];
+    float4 ks[kQaWarps][kQKeys];         // scales [pair of keys][group][key] of the warp's block, K ...
+    float4 vs[kQaWarps][kQKeys];         // ... and V
+    float size[kQaWarps][kQKeys];        // exponent of each key's largest V scale
+    float m[kQaWarps][8], l[kQaWarps][8];
+    uint32_t ws[kQaWarps + 1];
+    uint32_t pair, first;
+    int has[kQaWarps];
+};
+static_assert(8 * kQaCol * 4 <= kQBlock, "a warp's sums fit the block that it has consumed");
 
-__device__ __forceinline__ int64_t block_count(const QuantCache &c, int p) { return (quant_len(c, p) + kQKeys - 1) / kQKeys; }
+int quant_attend_workers(int num_sms) { return min(num_sms, kQMaxWorkers); }
+
+__device__ __forceinline__ uint32_t block_count(const QuantCache &c, int p) { return (uint32_t)(quant_len(c, p) + kQKeys - 1) / kQKeys; }
 
 // Sum of the block counts of pairs [0, end) over a CTA of NT threads.
 template <int NT>
-__device__ int64_t count_blocks(const QuantCache &c, int end, long long *s)
+__device__ uint32_t count_blocks(const QuantCache &c, int end, uint32_t *s)
 {
-    long long v = 0;
+    uint32_t v = 0;
     for (int p = threadIdx.x; p < end; p += NT) v += block_count(c, p);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    v = __reduce_add_sync(kFull, v);
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0;
@@ -34,103 +51,424 @@ __device__ int64_t count_blocks(const QuantCache &c, int end, long long *s)
     return v;
 }
 
-__global__ void __launch_bounds__(kQaThreads) k_quant_attend(QuantAttendArgs a)
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 4608 bytes from global to shared memory; completion counts on `bar`
+__device__ __forceinline__ void fetch_block(uint8_t *dst, const uint8_t *src, unsigned long long *bar)
 {
-    __shared__ float s_q[kMaxGroup][kD];
-    __shared__ float s_kv[kQKeys][kD + 1];
-    __shared__ float s_p[kMaxGroup][kQKeys];
-    __shared__ float s_m[kMaxGroup], s_l[kMaxGroup], s_c[kMaxGroup];
-    __shared__ long long s_sum[kQaThreads / 32];
-    const int tid = threadIdx.x, w = blockIdx.x, G = a.G;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(kQBlock) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+                 "l"(src), "r"(kQBlock), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Wait for a phase of `bar`; gives up after a bounded number of tries.
+__device__ __forceinline__ bool wait_block(unsigned long long *bar, uint32_t parity)
+{
+    for (int i = 0; i < (1 << 22); i++) {
+        uint32_t ok;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
+// d = c + a b: 16 x 16 times 16 x 8, halves in, fp32 sums
+__device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                         float c0, float c1, float c2, float c3)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ unsigned long long as_u64(float2 a)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 as_f2(unsigned long long a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(r);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float2 a)
+{
+    const __half2 h = __floats2half2_rn(a.x, a.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b)
+{
+    const __half2 h = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 halves(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2 *>(&a)); }
+__device__ __forceinline__ float bf16_lo(uint32_t a) { return __uint_as_float(a << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t a) { return __uint_as_float(a & 0xffff0000u); }
+
+// Two codes (the lower nibbles of a word's bytes 0 and 2) as halves c - 8:
+// 0x6400 | c is 1024 + c.  The upper nibbles give 16 (c - 8).
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return add_half2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return add_half2((w & 0x00f000f0u) | 0x64006400u, 0xe480e480u); }
+
+// The reference maximum may lag the true one by 2^kQaLag, and weights are
+// lifted by 2^kQaLift: at most 2^14, a half's range.  What a pair of halves
+// drops of a weight is then at most 2^-37 of the largest one, 2^-17 over a
+// million keys whose errors all point one way; each step of lag would double
+// that, and raising the reference takes 2% of the time without any.
+constexpr float kQaLag = 1.0f;
+constexpr float kQaLift = 13.0f;
+
+// Attention over a worker's blocks.
+//
+// A warp takes whole blocks of 32 keys from its own ring of bulk copies.
+// A mask, an or and an addition make matrix operands of two codes; the 16 of
+// the upper nibbles goes into q and the results.  (The bits of a code are a
+// subnormal half, c 2^-24, and would do without the addition, but products of
+// subnormals are summed with their leading zeros: errors of 2^-16.)
+//   logits  S^T[16 x 8] = q[16 x 16] K^T[16 x 8]: rows are heads (8..15: the
+//           low halves of fp32 q), columns keys, one accumulator per group of
+//           channels, then scaled by the group's scale.
+//   values  O^T[16 x 8] += V^T[16 x 16] w[16 x 8]: rows are channels, columns
+//           heads, w = p times the value scale of the rows' group.
+// A logit tile's fragment (head, two keys) is a value tile's weight fragment.
+// A weight is a pair of halves (22 bits; one would cost 2^-12): up to 4 heads
+// the low parts are the columns 4..7, else they are a second product.
+// The reference maximum is of logit + exponent of the key's largest value
+// scale, so that w, not p, is what stays within a half's range.
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs a)
+{
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    QaSmem &sm = *reinterpret_cast<QaSmem *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, G = a.G;
+    if (lane < kQaStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sm.bar[warp][lane])) : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     pdl_wait();
     pdl_trigger();
-    const int64_t total = count_blocks<kQaThreads>(a.c, a.c.bh, s_sum);
-    const int64_t share = quant_share(total, a.workers, kQaMinShare);
-    int64_t x = w * share;
-    const int64_t end = min(total, x + share);
-    if (x >= end) return;
-    int p = 0;
-    int64_t first = 0;                   // first block of pair p in the total
-    while (first + block_count(a.c, p) <= x) first += block_count(a.c, p++);
-    for (; x < end; p++) {
-        const int64_t nb = block_count(a.c, p);
-        const int n = quant_len(a.c, p);
-        const int64_t b0 = x - first, b1 = min(nb, end - first);
-        first += nb;
-        if (b0 >= b1) continue;
-        x += b1 - b0;
-        __syncthreads();
-        for (int i = tid; i < G * kD; i += kQaThreads) s_q[i / kD][i % kD] = ld_as_f32(a.q, (int64_t)p * G * kD + i, a.is_bf16);
-        if (tid < kMaxGroup) {
-            s_m[tid] = -INFINITY;
-            s_l[tid] = 0.0f;
+
+    // this worker's blocks [x0, end) of all, and the pair of the first
+    const uint32_t total = count_blocks<kQaThreads>(a.c, a.c.bh, sm.ws);
+    const uint32_t share = (uint32_t)quant_share(total, a.workers, kQaMinShare);
+    const uint32_t x0 = blockIdx.x * share;
+    if (x0 >= total) return;
+    const uint32_t end = min(total, x0 + share);
+    for (uint32_t base = 0, c = 0;; c += kQaThreads) {
+        const uint32_t v = c + tid < (uint32_t)a.c.bh ? block_count(a.c, c + tid) : 0u;
+        uint32_t sum;
+        const uint32_t before = base + block_excl_scan<kQaThreads>(v, sm.ws, &sum);
+        if (x0 >= before && x0 - before < v) {
+            sm.pair = c + tid;
+            sm.first = before;
         }
-        float acc[kMaxGroup];
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; g++) acc[g] = 0.0f;
-        for (int64_t b = b0; b < b1; b++) {
-            const uint8_t *blk = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
-            const int valid = (int)min((int64_t)kQKeys, n - b * kQKeys);
-            __syncthreads();
-            const int c = tid, r = c >> 5, t = (c & 31) >> 3, i = c & 7;
-            for (int j = 0; j < kQKeys; j++) {
-                const int nib = 32 * t + 8 * r + i;
-                const float s = bf16_bits_f32(reinterpret_cast<const uint16_t *>(blk + kQOffKs)[4 * j + r]);
-                s_kv[j][c] = j < valid ? (float)((blk[j * kQRow + nib / 2] >> (4 * (nib & 1)) & 15) - 8) * s : 0.0f;
-            }
-            __syncthreads();
-            for (int e = tid; e < G * kQKeys; e += kQaThreads) {
-                const int g = e / kQKeys, j = e % kQKeys;
-                float z = 0.0f;
-                for (int d = 0; d < kD; d++) z = fmaf(s_q[g][d], s_kv[j][d], z);
-                z *= a.scale2;
-                s_p[g][j] = j < valid ? z : -INFINITY;
-                if (a.logits) a.logits[(((int64_t)p * (a.c.n_cap / kQKeys) + b) * G + g) * kQKeys + j] = z;
-            }
-            __syncthreads();
-            if (tid < G) {
-                float m = s_m[tid];
-                for (int j = 0; j < kQKeys; j++) m = fmaxf(m, s_p[tid][j]);
-                const float ref = m == -INFINITY ? 0.0f : m;
-                s_c[tid] = exp2f(s_m[tid] - ref);
-                float l = s_l[tid] * s_c[tid];
-                for (int j = 0; j < kQKeys; j++) l += s_p[tid][j] = exp2f(s_p[tid][j] - ref);
-                s_l[tid] = l;
-                s_m[tid] = m;
-            }
-            for (int j = 0; j < kQKeys; j++) {
-                const int nib = 16 * (i ^ v_turn(j)) + 4 * r + t;      // channel 32 r + 8 t + i
-                const float s = bf16_bits_f32(reinterpret_cast<const uint16_t *>(blk + kQOffVs)[4 * j + r]);
-                s_kv[j][c] = j < valid ? (float)((blk[kQOffV + j * kQRow + nib / 2] >> (4 * (nib & 1)) & 15) - 8) * s : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int g = 0; g < kMaxGroup; g++) {
-                if (g >= G) break;
-                float o = acc[g] * s_c[g];
-                for (int j = 0; j < valid; j++) o = fmaf(s_p[g][j], s_kv[j][tid], o);
-                acc[g] = o;
-            }
-        }
-        float *part = a.part + (int64_t)(p + w) * G * kQPart;
-        __syncthreads();
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; g++) {
-            if (g >= G) break;
-            part[g * kQPart + tid] = acc[g];
-            if (tid == 0) {
-                part[g * kQPart + kD] = s_m[g];
-                part[g * kQPart + kD + 1] = s_l[g];
-            }
-        }
+        base += sum;
+        if (base > x0) break;
     }
+    __syncthreads();
+    int p = (int)sm.pair;
+    uint32_t first = sm.first;           // first block of pair p
+    const int64_t pair_blocks = a.c.n_cap / kQKeys;
+
+    // the warp's blocks are x = warp (mod kQaWarps); copies run ahead of x
+    uint32_t x = x0 + (warp + kQaWarps - x0 % kQaWarps) % kQaWarps;
+    uint32_t fx = x, ffirst = first, fnb = block_count(a.c, p);
+    int fp = p;
+    auto fetch = [&](int s) {
+        if (fx >= end) return;
+        while (fx - ffirst >= fnb) {
+            ffirst += fnb;
+            fnb = block_count(a.c, ++fp);
+        }
+        if (lane == 0) fetch_block(sm.ring[warp][s], a.c.blocks + (fp * pair_blocks + (fx - ffirst)) * kQBlock, &sm.bar[warp][s]);
+        fx += kQaWarps;
+    };
+#pragma unroll 1
+    for (int s = 0; s < kQaStages; s++) fetch(s);
+    int slot = 0;
+    uint32_t parity = 0;
+    bool late = false;
+    const int head = WIDE ? g : (g & 3);
+    const float low = !WIDE && g >= 4 ? -1.0f : 0.0f;   // this column holds the weights' low parts
+
+    for (uint32_t nb; first < end; first += nb, p++) {
+        nb = block_count(a.c, p);
+        const uint32_t stop = min(end, first + nb);
+        if (nb == 0 || first + nb <= x0) continue;
+        const int n = quant_len(a.c, p);
+        const bool has = x < stop;
+        float2 o[4][4];                  // channels 32r + {0, 16, 8, 24} + g, heads 2t and 2t + 1
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.0f, 0.0f);
+        int free_slot = -1;
+        if (has) {
+            // q of the head, scaled by a power of two to at most 2^14, as halves: qa[group][8 channels 8t..]
+            uint32_t qh[4][4], ql[4][4];
+            float qscale;
+            {
+                float v[4][8], top = 0.0f;
+                const int64_t base = ((int64_t)p * G + head) * kD + 8 * t;
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        v[r][i] = head < G ? ld_as_f32(a.q, base + 32 * r + i, BF16) : 0.0f;
+                        top = fmaxf(top, fabsf(v[r][i]));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                // 2^(13 - exponent of top), within fp32's normal range, and its inverse
+                const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 254);
+                const float up = __uint_as_float((uint32_t)(267 - e) << 23);
+                qscale = a.scale2 * __uint_as_float((uint32_t)(e - 13) << 23);
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    float hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float y = v[r][i] * up;
+                        hi[i] = __half2float(__float2half_rn(y));
+                        lo[i] = BF16 ? 0.0f : __half2float(__float2half_rn(y - hi[i]));
+                        if (i & 1) {     // odd nibbles come 16 times as large
+                            hi[i] *= 0.0625f;
+                            lo[i] *= 0.0625f;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        qh[r][i] = pack_half2(make_float2(hi[i], hi[i + 4]));
+                        ql[r][i] = pack_half2(make_float2(lo[i], lo[i + 4]));
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int h = 0; h < 4; h++) o[r][h] = make_float2(0.0f, 0.0f);
+
+#pragma unroll 1
+            for (; x < stop; x += kQaWarps) {
+                uint8_t *blk = sm.ring[warp][slot];
+                if (!wait_block(&sm.bar[warp][slot], parity)) late = true;
+                const int b = (int)(x - first), valid = min(kQKeys, n - b * kQKeys);
+                {   // scales as fp32 (zero behind the length), two groups of two keys a lane
+                    const int pair = lane >> 1, half = lane & 1;
+                    uint2 k = make_uint2(0, 0), v = make_uint2(0, 0);
+                    const uint32_t *sk = reinterpret_cast<const uint32_t *>(blk + kQOffKs) + 4 * pair + half;
+                    const uint32_t *sv = reinterpret_cast<const uint32_t *>(blk + kQOffVs) + 4 * pair + half;
+                    if (2 * pair < valid) k.x = sk[0], v.x = sv[0];
+                    if (2 * pair + 1 < valid) k.y = sk[2], v.y = sv[2];
+                    sm.ks[warp][lane] = make_float4(bf16_lo(k.x), bf16_lo(k.y), bf16_hi(k.x), bf16_hi(k.y));
+                    sm.vs[warp][lane] = make_float4(bf16_lo(v.x), bf16_lo(v.y), bf16_hi(v.x), bf16_hi(v.y));
+                    // exponents, 0 for those of infinities and NaN
+                    uint32_t ex = (v.x >> 7) & 0x00ff00ffu, ey = (v.y >> 7) & 0x00ff00ffu;
+                    ex &= ~((((ex + 0x00010001u) >> 8) & 0x00010001u) * 255u);
+                    ey &= ~((((ey + 0x00010001u) >> 8) & 0x00010001u) * 255u);
+                    uint32_t e = __vmaxu2(__byte_perm(ex, ey, 0x5410), __byte_perm(ex, ey, 0x7632));   // (key, key + 1)
+                    e = __vmaxu2(e, __shfl_xor_sync(kFull, e, 1));
+                    sm.size[warp][lane] = fmaxf((float)((int)((e >> (16 * half)) & 0xffffu) - 126), -80.0f);
+                    __syncwarp();
+                }
+                float2 z[4];             // keys 8i + 2t, + 1
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint4 kc = *reinterpret_cast<const uint4 *>(blk + (8 * i + g) * kQRow + 16 * t);
+                    const float4 s01 = sm.ks[warp][2 * (4 * i + t)], s23 = sm.ks[warp][2 * (4 * i + t) + 1];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const uint32_t w = r == 0 ? kc.x : r == 1 ? kc.y : r == 2 ? kc.z : kc.w, w8 = w >> 8;
+                        float d[4];
+                        mma16816(d, qh[r][0], BF16 ? 0u : ql[r][0], qh[r][1], BF16 ? 0u : ql[r][1], codes_lo(w), codes_hi(w), 0.0f, 0.0f, 0.0f, 0.0f);
+                        mma16816(d, qh[r][2], BF16 ? 0u : ql[r][2], qh[r][3], BF16 ? 0u : ql[r][3], codes_lo(w8), codes_hi(w8), d[0], d[1], d[2], d[3]);
+                        float2 x = make_float2(d[0], d[1]);
+                        if (!BF16) x = add2(x, make_float2(d[2], d[3]));
+                        const float2 sc = r == 0 ? make_float2(s01.x, s01.y) : r == 1 ? make_float2(s01.z, s01.w)
+                                        : r == 2 ? make_float2(s23.x, s23.y) : make_float2(s23.z, s23.w);
+                        z[i] = r ? fma2(x, sc, z[i]) : mul2(x, sc);
+                    }
+                    z[i] = mul2(z[i], make_float2(qscale, qscale));
+                }
+                if (a.logits && g < G) {
+                    float *zo = a.logits + ((p * pair_blocks + b) * G + g) * kQKeys + 2 * t;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) *reinterpret_cast<float2 *>(zo + 8 * i) = z[i];
+                }
+                if (valid < kQKeys) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (8 * i + 2 * t >= valid) z[i].x = -INFINITY;
+                        if (8 * i + 2 * t + 1 >= valid) z[i].y = -INFINITY;
+                    }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float2 e = add2(z[i], *reinterpret_cast<const float2 *>(&sm.size[warp][8 * i + 2 * t]));
+                    top = fmaxf(top, fmaxf(e.x, e.y));
+                }
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                if (__any_sync(kFull, top > m + kQaLag)) {     // rare: raise the reference maximum
+                    const float to = top > m + kQaLag ? top : m;
+                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+                    m = to;
+                    l2 = mul2(l2, make_float2(f, f));
+                    const float2 fc = make_float2(__shfl_sync(kFull, f, 8 * t), __shfl_sync(kFull, f, 8 * t + 4));
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int h = 0; h < 4; h++) o[r][h] = mul2(o[r][h], fc);
+                }
+                const float off = m == -INFINITY ? 0.0f : kQaLift - m;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    z[i] = add2(z[i], make_float2(off, off));
+                    z[i] = make_float2(ex2(z[i].x), ex2(z[i].y));
+                    l2 = add2(l2, z[i]);
+                }
+                uint2 vc[2][4];          // codes of the keys 16u + 2t, + 1, + 8, + 9
+#pragma unroll
+                for (int u = 0; u < 2; u++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const int key = 16 * u + 8 * (k >> 1) + 2 * t + (k & 1);
+                        vc[u][k] = *reinterpret_cast<const uint2 *>(blk + kQOffV + key * kQRow + 8 * (g ^ v_turn(key)));
+                    }
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    float d[2][4];
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        uint32_t bw[2], bl[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float2 sc = reinterpret_cast<const float2 *>(&sm.vs[warp][2 * (8 * u + 4 * k + t)])[r];
+                            const float2 w = mul2(z[2 * u + k], sc);
+                            const uint32_t hi = pack_half2(w);
+                            if (WIDE) {
+                                bw[k] = hi;
+                                bl[k] = pack_half2(fma2(halves(hi), make_float2(-1.0f, -1.0f), w));
+                            } else {
+                                bw[k] = pack_half2(fma2(halves(hi), make_float2(low, low), w));
+                            }
+                        }
+                        // codes of the group's channels: halves (key 2t, key 2t + 1), and the keys 8 further
+                        const uint32_t sel = (r & 1) ? 0x7632u : 0x5410u;
+                        const uint32_t v0 = __byte_perm(r < 2 ? vc[u][0].x : vc[u][0].y, r < 2 ? vc[u][1].x : vc[u][1].y, sel);
+                        const uint32_t v1 = __byte_perm(r < 2 ? vc[u][2].x : vc[u][2].y, r < 2 ? vc[u][3].x : vc[u][3].y, sel);
+                        const uint32_t a0 = codes_lo(v0), a1 = codes_lo(v0 >> 8), a2 = codes_lo(v1), a3 = codes_lo(v1 >> 8);
+                        const uint32_t c0 = codes_hi(v0), c1 = codes_hi(v0 >> 8), c2 = codes_hi(v1), c3 = codes_hi(v1 >> 8);
+                        // matrix instructions cut their sums: a block's only, which are then added with rounding
+                        mma16816(d[0], a0, a1, a2, a3, bw[0], bw[1], u ? d[0][0] : 0.0f, u ? d[0][1] : 0.0f, u ? d[0][2] : 0.0f, u ? d[0][3] : 0.0f);
+                        mma16816(d[1], c0, c1, c2, c3, bw[0], bw[1], u ? d[1][0] : 0.0f, u ? d[1][1] : 0.0f, u ? d[1][2] : 0.0f, u ? d[1][3] : 0.0f);
+                        if (WIDE) {
+                            mma16816(d[0], a0, a1, a2, a3, bl[0], bl[1], d[0][0], d[0][1], d[0][2], d[0][3]);
+                            mma16816(d[1], c0, c1, c2, c3, bl[0], bl[1], d[1][0], d[1][1], d[1][2], d[1][3]);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        o[r][2 * h] = add2(o[r][2 * h], make_float2(d[h][0], d[h][1]));
+                        o[r][2 * h + 1] = add2(o[r][2 * h + 1], make_float2(d[h][2], d[h][3]));
+                    }
+                }
+                __syncwarp();
+                if (x + kQaWarps < stop) fetch(slot);
+                else free_slot = slot;   // its block holds the warp's sums until they are merged
+                if (++slot == kQaStages) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
+            }
+            // sums into the block consumed last: [column][channel]
+            float *so = reinterpret_cast<float *>(sm.ring[warp][free_slot]);
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int h = 0; h < 4; h++) {
+                    const int c = 32 * r + 16 * (h & 1) + 8 * (h >> 1) + g;
+                    so[2 * t * kQaCol + c] = o[r][h].x * (h >> 1 ? 0.0625f : 1.0f);
+                    so[(2 * t + 1) * kQaCol + c] = o[r][h].y * (h >> 1 ? 0.0625f : 1.0f);
+                }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            float l = l2.x + l2.y;
+            l += __shfl_xor_sync(kFull, l, 1);
+            l += __shfl_xor_sync(kFull, l, 2);
+            if (t == 0) {
+                sm.m[warp][g] = m;
+                sm.l[warp][g] = l;
+            }
+        }
+        if (lane == 0) sm.has[warp] = has ? free_slot : -1;
+        __syncthreads();
+        float *part = a.part + (int64_t)(p + blockIdx.x) * G * kQPart;
+        for (int e = tid; e < G * kD; e += kQaThreads) {
+            const int h = e / kD, c = e % kD;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kQaWarps; w++)
+                if (sm.has[w] >= 0) top = fmaxf(top, sm.m[w][h]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f, ls = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kQaWarps; w++)
+                if (sm.has[w] >= 0) {
+                    const float *so = reinterpret_cast<const float *>(sm.ring[w][sm.has[w]]);
+                    const float f = ex2(sm.m[w][h] - ref);
+                    sum = fmaf(f, WIDE ? so[h * kQaCol + c] : so[h * kQaCol + c] + so[(h + 4) * kQaCol + c], sum);
+                    ls = fmaf(f, sm.l[w][h], ls);
+                }
+            part[h * kQPart + c] = sum;
+            if (c == 0) {
+                part[h * kQPart + kD] = top - kQaLift;
+                part[h * kQPart + kD + 1] = ls;
+            }
+        }
+        __syncthreads();
+        if (free_slot >= 0) fetch(free_slot);
+    }
+    if (late && lane == 0 && a.c.status && atomicCAS(a.c.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.c.status[1] = p;
 }
 
 // Merge of a pair's partial results (CTAs x < G: head x) and its part of acc
 // (CTAs x >= G: keys [(x - G) kQmKeys, ...)).
 __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
 {
-    __shared__ long long s_sum[kQmThreads / 32];
+    __shared__ uint32_t s_sum[kQmThreads / 32];
     __shared__ float s_lse[kMaxGroup];
     const int tid = threadIdx.x, p = blockIdx.y, G = a.G;
     pdl_wait();
@@ -144,9 +482,9 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
         if (tid == 0 && a.lse) a.lse[(int64_t)p * G + blockIdx.x] = -INFINITY;
         return;
     }
-    const int64_t total = count_blocks<kQmThreads>(a.c, a.c.bh, s_sum);
-    const int64_t first = count_blocks<kQmThreads>(a.c, p, s_sum);
-    const int64_t share = quant_share(total, a.workers, kQaMinShare);
+    const uint32_t total = count_blocks<kQmThreads>(a.c, a.c.bh, s_sum);
+    const uint32_t first = count_blocks<kQmThreads>(a.c, p, s_sum);
+    const uint32_t share = (uint32_t)quant_share(total, a.workers, kQaMinShare);
     const int w0 = (int)(first / share), w1 = (int)((first + block_count(a.c, p) - 1) / share);
     const float *part = a.part + (int64_t)(p + w0) * G * kQPart;
     const int ns = w1 - w0 + 1;
@@ -186,7 +524,12 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
 
 cudaError_t launch_quant_attend(const QuantAttendArgs &a, cudaStream_t s)
 {
-    cudaError_t e = launch_pdl(k_quant_attend, dim3(a.workers), dim3(kQaThreads), 0, s, a);
+    static std::atomic<int> done[4][kMaxDevices];
+    const int kind = (a.is_bf16 ? 2 : 0) + (a.G > 4 ? 1 : 0);
+    auto kern = kind == 3 ? k_quant_attend<true, true> : kind == 2 ? k_quant_attend<true, false>
+              : kind == 1 ? k_quant_attend<false, true> : k_quant_attend<false, false>;
+    cudaError_t e = dyn_smem_limit(kern, (int)sizeof(QaSmem), done[kind]);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(a.workers), dim3(kQaThreads), sizeof(QaSmem), s, a);
     if (e != cudaSuccess) return e;
     const unsigned parts = a.accumulate ? (unsigned)((a.c.n_cap + kQmKeys - 1) / kQmKeys) : 0u;
     return launch_pdl(k_quant_merge, dim3(a.G + parts, a.c.bh), dim3(kQmThreads), 0, s, a);

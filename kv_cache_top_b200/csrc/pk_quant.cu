@@ -8,8 +8,9 @@ using namespace pk;
 
 namespace {
 
-// Device memory of the current device, or page-locked / managed host memory.
-bool quant_accessible(const void *ptr, size_t align)
+// Device memory of the current device, or (unless `device_only`) page-locked /
+// managed host memory.
+bool quant_accessible(const void *ptr, size_t align, bool device_only = false)
 {
     cudaPointerAttributes at;
     if (!ptr || ((uintptr_t)ptr % align) != 0) return false;
@@ -21,7 +22,7 @@ bool quant_accessible(const void *ptr, size_t align)
         int dev = -1;
         return cudaGetDevice(&dev) == cudaSuccess && at.device == dev;
     }
-    return at.type == cudaMemoryTypeHost || at.type == cudaMemoryTypeManaged;
+    return !device_only && (at.type == cudaMemoryTypeHost || at.type == cudaMemoryTypeManaged);
 }
 
 pk_status quant_status(cudaError_t e)
@@ -45,9 +46,9 @@ pk_status check_cache(const pk_quant_cache *c, QuantCache *out)
 {
     const pk_status st = check_sizes(c);
     if (st != PK_OK) return st;
-    if (!quant_accessible(c->blocks, 16) || !quant_accessible(c->lens, 4)) return PK_ERR_INVALID_ARG;
-    if (c->acc && !quant_accessible(c->acc, 4)) return PK_ERR_INVALID_ARG;
-    if (c->status && !quant_accessible(c->status, 4)) return PK_ERR_INVALID_ARG;
+    if (!quant_accessible(c->blocks, 16, true) || !quant_accessible(c->lens, 4, true)) return PK_ERR_INVALID_ARG;
+    if (c->acc && !quant_accessible(c->acc, 4, true)) return PK_ERR_INVALID_ARG;
+    if (c->status && !quant_accessible(c->status, 4, true)) return PK_ERR_INVALID_ARG;
     *out = QuantCache{(uint8_t *)c->blocks, c->lens, c->acc, c->status, c->n_cap, c->bh};
     return PK_OK;
 }
@@ -131,7 +132,7 @@ pk_status pk_quant_attend(const pk_quant_cache *cache, const void *q, int32_t gr
     if (st != PK_OK) return st;
     if (!(scale >= 0.0f) || std::isinf(scale) || (accumulate && !cache->acc)) return PK_ERR_INVALID_ARG;
     if (!quant_accessible(q, cache->kv_dtype == PK_BF16 ? 2 : 4) || !quant_accessible(out, 4) ||
-        (lse && !quant_accessible(lse, 4)) || !quant_accessible(work, 256))
+        (lse && !quant_accessible(lse, 4)) || !quant_accessible(work, 256, true))
         return PK_ERR_INVALID_ARG;
     if (work_bytes < need) return PK_ERR_CAPACITY;
     int dev = 0, sms = 148;

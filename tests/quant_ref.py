@@ -86,7 +86,11 @@ def attend(q, K, V, scale=None):
     relative at most), summed in fp32 by instructions that may cut instead of round (2 U a step, 136 steps), scaled
     by a few rounded factors: |dz| <= (2 * 136 U + 2^-21) S, S = scale sum |q||k|; z itself is rounded to fp32 in
     log2 units (2 U |z|, also of the maximum).  A weight's relative error is then e = 2 (dz) + 2^-21 (the two
-    exponentials).  Sums over n keys: steps of 16 keys that may cut (2 U each), else rounding, six sigma."""
+    exponentials).  Sums over n keys: steps of 16 keys that may cut (2 U each), else rounding, six sigma.
+    A product p s of a weight and a group's scale is held as a pair of halves lifted by 2^13 over a reference at most
+    2 max(p s), so it is off by at most 2^-25 of that unit, 2^-37 max(p s), beside the 2^-22 relative that e covers;
+    with |code - 8| <= 7 the n keys give at most 7 n 2^-37 max(p s).  s of a key is its largest |V| / 7 (pack() makes the
+    largest code of a group +-7)."""
     n = len(K)
     scale = 1 / math.sqrt(D) if scale is None else scale
     if n == 0:
@@ -102,7 +106,8 @@ def attend(q, K, V, scale=None):
     sums = U * (n / 8 + 6 * math.sqrt(n))
     rel = 2 * dz + 2.0 ** -20 + sums
     out = p @ V
-    return out, (np.log(total) + top)[:, 0], p, (p @ np.abs(V)) * rel[:, None] + 1e-37, rel + 2 * U * np.abs(top[:, 0]), rel
+    held = n * 2.0 ** -37 * (p * np.abs(V).max(1)).max(1, keepdims=True)
+    return out, (np.log(total) + top)[:, 0], p, (p @ np.abs(V)) * rel[:, None] + held + 1e-37, rel + 2 * U * np.abs(top[:, 0]), rel
 
 
 def evict(acc, n, budget, sink, recent):

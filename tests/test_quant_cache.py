@@ -376,6 +376,22 @@ def test_attend_values_of_mixed_size(pk):
 
 
 @gpu
+def test_attend_long_tail_of_small_weights(pk):
+    """One key 2^24 heavier than each of 300000 others whose values all point one way: the tail's share counts."""
+    n, cap = 300001, 300032
+    rng = np.random.default_rng(18)
+    K, V = make_rows(rng, 64, torch.float32, 1e-3).numpy(), np.abs(make_rows(rng, 64, torch.float32).numpy())
+    q = np.full((1, D), 0.5, np.float32)
+    K[0] = 24 * math.log(2) * math.sqrt(D) / (0.5 * D)       # logit 24 ln 2; the others about 0
+    K[32] = K[33]
+    V[0] = 1
+    two = ref.pack(K, V)
+    blocks = np.concatenate([two[:1], np.repeat(two[1:], cap // KEYS - 1, 0)])[None]
+    c = pk.pk_quant_view(torch.from_numpy(blocks).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), pk.PK_F32)
+    check_attend(pk, c, blocks, [n], torch.from_numpy(q)[None].cuda(), 1)
+
+
+@gpu
 def test_attend_nan_stays_in_its_group_of_values(pk):
     """A NaN group of V makes its 32 channels NaN and no others; a NaN group of K makes all of the pair NaN; rows
     behind the length (0xff bytes) and other pairs do not matter."""
