@@ -11,9 +11,9 @@
 
 namespace pk {
 
-constexpr int kQaWarps = 12;
+constexpr int kQaWarps = 16;
 constexpr int kQaThreads = 32 * kQaWarps;
-constexpr int kQaStages = 3;             // blocks in flight per warp
+constexpr int kQaStages = 2;             // blocks in flight per warp
 constexpr int kQaMinShare = kQaWarps;    // blocks a worker takes at least: one per warp
 constexpr int kQaCol = kD + 4;           // floats between the columns of a warp's sums in shared memory
 constexpr int kQmThreads = 256;          // merge kernel
@@ -88,6 +88,20 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
+// d = c + a b: 16 x 32 times 32 x 8, signed bytes in, 32-bit sums.  The sums
+// start at kQaMagic, the bits of 1.5 2^23: read as fp32 they are 1.5 2^23 + the
+// sum (below 2^22), so no conversion is needed.
+constexpr uint32_t kQaMagic = 0x4b400000u;
+__device__ __forceinline__ void imma16832(float2 d[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    uint32_t x, y, z, w;
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kQaMagic));
+    d[0] = make_float2(__uint_as_float(x), __uint_as_float(y));
+    d[1] = make_float2(__uint_as_float(z), __uint_as_float(w));
+}
+
 // two fp32 operations in one instruction
 __device__ __forceinline__ unsigned long long as_u64(float2 a)
 {
@@ -132,19 +146,22 @@ __device__ __forceinline__ uint32_t pack_half2(float2 a)
     const __half2 h = __floats2half2_rn(a.x, a.y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b)
-{
-    const __half2 h = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ float2 halves(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2 *>(&a)); }
 __device__ __forceinline__ float bf16_lo(uint32_t a) { return __uint_as_float(a << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t a) { return __uint_as_float(a & 0xffff0000u); }
 
-// Two codes (the lower nibbles of a word's bytes 0 and 2) as halves c - 8:
-// 0x6400 | c is 1024 + c.  The upper nibbles give 16 (c - 8).
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return add_half2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return add_half2((w & 0x00f000f0u) | 0x64006400u, 0xe480e480u); }
+// Two codes (nibble 0, or 1, of the bytes 0 and 2) as halves (c - 8) 2^-9: the
+// bits c are the subnormal half c 2^-24, the upper nibble's 16 c 2^-24; one
+// exact multiply-add makes either normal.
+constexpr float kQaUnit = 512.0f;
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return fma_half2(w & 0x000f000fu, 0x78007800u, 0xa400a400u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return fma_half2(w & 0x00f000f0u, 0x68006800u, 0xa400a400u); }
 
 // The reference maximum may lag the true one by 2^kQaLag, and weights are
 // lifted by 2^kQaLift: at most 2^14, a half's range.  What a pair of halves
@@ -157,13 +174,14 @@ constexpr float kQaLift = 13.0f;
 // Attention over a worker's blocks.
 //
 // A warp takes whole blocks of 32 keys from its own ring of bulk copies.
-// A mask, an or and an addition make matrix operands of two codes; the 16 of
-// the upper nibbles goes into q and the results.  (The bits of a code are a
-// subnormal half, c 2^-24, and would do without the addition, but products of
+// A mask and a multiply-add make matrix operands of two codes.  (The masked
+// bits are subnormal halves and would do as they are, but products of
 // subnormals are summed with their leading zeros: errors of 2^-16.)
-//   logits  S^T[16 x 8] = q[16 x 16] K^T[16 x 8]: rows are heads (8..15: the
-//           low halves of fp32 q), columns keys, one accumulator per group of
-//           channels, then scaled by the group's scale.
+//   logits  S^T[16 x 8] = q[16 x 32] K^T[32 x 8] of bytes: rows are digits of
+//           the heads' q, columns keys, one product per group of channels,
+//           whose digits are joined and scaled by the group's scale.  Bytes
+//           take 3 instructions for 8 codes (halves 9) and half the products,
+//           and the sums are exact.
 //   values  O^T[16 x 8] += V^T[16 x 16] w[16 x 8]: rows are channels, columns
 //           heads, w = p times the value scale of the rows' group.
 // A logit tile's fragment (head, two keys) is a value tile's weight fragment.
@@ -171,7 +189,7 @@ constexpr float kQaLift = 13.0f;
 // the low parts are the columns 4..7, else they are a second product.
 // The reference maximum is of logit + exponent of the key's largest value
 // scale, so that w, not p, is what stays within a half's range.
-template <bool BF16, bool WIDE>
+template <bool WIDE>
 __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs a)
 {
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -225,6 +243,10 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     const int head = WIDE ? g : (g & 3);
     const float low = !WIDE && g >= 4 ? -1.0f : 0.0f;   // this column holds the weights' low parts
 
+    // x = high_digit d[0] + low_digit d[1] (+ 2^-16 d'[0]) without the sums' 1.5 2^23: every step but the last is exact
+    const float high_digit = WIDE || g < 4 ? 1.0f : 0x1p-8f, low_digit = WIDE ? 0x1p-8f : high_digit * 0x1p-16f;
+    const float start = -12582912.0f * (high_digit + low_digit + (WIDE ? 0x1p-16f : 0.0f));
+
     for (uint32_t nb; first < end; first += nb, p++) {
         nb = block_count(a.c, p);
         const uint32_t stop = min(end, first + nb);
@@ -236,42 +258,45 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         float2 l2 = make_float2(0.0f, 0.0f);
         int free_slot = -1;
         if (has) {
-            // q of the head, scaled by a power of two to at most 2^14, as halves: qa[group][8 channels 8t..]
-            uint32_t qh[4][4], ql[4][4];
+            // q of the head as 32-bit fixed point of its largest magnitude, in signed bytes: digit k of channels
+            // 32r + 8t + {0, 2, 4, 6} and {1, 3, 5, 7}.  A product's rows g and g + 8 hold digits 0 and 1, and 2 (WIDE), or
+            // g / 4 and g / 4 + 2
+            uint32_t qd[4][WIDE ? 6 : 4];
             float qscale;
             {
-                float v[4][8], top = 0.0f;
+                float v[4][8];
+                uint32_t top = 0;
                 const int64_t base = ((int64_t)p * G + head) * kD + 8 * t;
 #pragma unroll
                 for (int r = 0; r < 4; r++)
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
-                        v[r][i] = head < G ? ld_as_f32(a.q, base + 32 * r + i, BF16) : 0.0f;
-                        top = fmaxf(top, fabsf(v[r][i]));
+                        v[r][i] = head < G ? ld_as_f32(a.q, base + 32 * r + i, a.is_bf16) : 0.0f;
+                        top = max(top, __float_as_uint(v[r][i]) & 0x7fffffffu);
                     }
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-                // 2^(13 - exponent of top), within fp32's normal range, and its inverse
-                const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 254);
-                const float up = __uint_as_float((uint32_t)(267 - e) << 23);
-                qscale = a.scale2 * __uint_as_float((uint32_t)(e - 13) << 23);
+                top = max(top, __shfl_xor_sync(kFull, top, 1));
+                top = max(top, __shfl_xor_sync(kFull, top, 2));
+                // q 2^(156 - e) is below 2^30; a product is 16 (code - 8) times a digit of weight 2^24.  A query with an
+                // infinity or NaN has NaN logits
+                const uint32_t e = min(max(top >> 23, 30u), 254u);
+                const float up = __uint_as_float((283u - e) << 23);
+                qscale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a.scale2 * __uint_as_float((e - 9u) << 23);
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    float hi[8], lo[8];
+                    uint32_t d[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float y = v[r][i] * up;
-                        hi[i] = __half2float(__float2half_rn(y));
-                        lo[i] = BF16 ? 0.0f : __half2float(__float2half_rn(y - hi[i]));
-                        if (i & 1) {     // odd nibbles come 16 times as large
-                            hi[i] *= 0.0625f;
-                            lo[i] *= 0.0625f;
-                        }
-                    }
+                    for (int i = 0; i < 8; i++)      // bytes 3, 2, 1, 0: digits 0, 1, 2, 3
+                        d[i] = ((uint32_t)__float2int_rn(v[r][i] * up) + 0x00808080u) ^ 0x00808080u;
+                    const int first = WIDE ? 3 : 3 - (g >> 2), second = WIDE ? 2 : 1 - (g >> 2);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        qh[r][i] = pack_half2(make_float2(hi[i], hi[i + 4]));
-                        ql[r][i] = pack_half2(make_float2(lo[i], lo[i + 4]));
+                    for (int h = 0; h < 2; h++) {
+                        auto digit = [&](int k) {
+                            const uint32_t s = (uint32_t)k | (uint32_t)(k + 4) << 4;
+                            return __byte_perm(__byte_perm(d[h], d[h + 2], s), __byte_perm(d[h + 4], d[h + 6], s), 0x5410);
+                        };
+                        qd[r][2 * h] = digit(first);
+                        qd[r][2 * h + 1] = digit(second);
+                        if (WIDE) qd[r][4 + h] = digit(1);
                     }
                 }
             }
@@ -310,16 +335,20 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
                     const float4 s01 = sm.ks[warp][2 * (4 * i + t)], s23 = sm.ks[warp][2 * (4 * i + t) + 1];
 #pragma unroll
                     for (int r = 0; r < 4; r++) {
-                        const uint32_t w = r == 0 ? kc.x : r == 1 ? kc.y : r == 2 ? kc.z : kc.w, w8 = w >> 8;
-                        float d[4];
-                        mma16816(d, qh[r][0], BF16 ? 0u : ql[r][0], qh[r][1], BF16 ? 0u : ql[r][1], codes_lo(w), codes_hi(w), 0.0f, 0.0f, 0.0f, 0.0f);
-                        mma16816(d, qh[r][2], BF16 ? 0u : ql[r][2], qh[r][3], BF16 ? 0u : ql[r][3], codes_lo(w8), codes_hi(w8), d[0], d[1], d[2], d[3]);
-                        float2 x = make_float2(d[0], d[1]);
-                        if (!BF16) x = add2(x, make_float2(d[2], d[3]));
+                        const uint32_t w = r == 0 ? kc.x : r == 1 ? kc.y : r == 2 ? kc.z : kc.w;
+                        const uint32_t b0 = ((w << 4) & 0xf0f0f0f0u) ^ 0x80808080u, b1 = (w & 0xf0f0f0f0u) ^ 0x80808080u;   // 16 (code - 8)
+                        float2 d[2], x;
+                        imma16832(d, qd[r][0], qd[r][1], qd[r][2], qd[r][3], b0, b1);
+                        x = fma2(d[1], make_float2(low_digit, low_digit), fma2(d[0], make_float2(high_digit, high_digit), make_float2(start, start)));
+                        if (WIDE) {
+                            imma16832(d, qd[r][4], 0u, qd[r][5], 0u, b0, b1);
+                            x = fma2(d[0], make_float2(0x1p-16f, 0x1p-16f), x);
+                        }
                         const float2 sc = r == 0 ? make_float2(s01.x, s01.y) : r == 1 ? make_float2(s01.z, s01.w)
                                         : r == 2 ? make_float2(s23.x, s23.y) : make_float2(s23.z, s23.w);
                         z[i] = r ? fma2(x, sc, z[i]) : mul2(x, sc);
                     }
+                    if (!WIDE) z[i] = add2(z[i], make_float2(__shfl_xor_sync(kFull, z[i].x, 16), __shfl_xor_sync(kFull, z[i].y, 16)));
                     z[i] = mul2(z[i], make_float2(qscale, qscale));
                 }
                 if (a.logits && g < G) {
@@ -421,8 +450,8 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
 #pragma unroll
                 for (int h = 0; h < 4; h++) {
                     const int c = 32 * r + 16 * (h & 1) + 8 * (h >> 1) + g;
-                    so[2 * t * kQaCol + c] = o[r][h].x * (h >> 1 ? 0.0625f : 1.0f);
-                    so[(2 * t + 1) * kQaCol + c] = o[r][h].y * (h >> 1 ? 0.0625f : 1.0f);
+                    so[2 * t * kQaCol + c] = o[r][h].x * kQaUnit;
+                    so[(2 * t + 1) * kQaCol + c] = o[r][h].y * kQaUnit;
                 }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             float l = l2.x + l2.y;
@@ -524,10 +553,9 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
 
 cudaError_t launch_quant_attend(const QuantAttendArgs &a, cudaStream_t s)
 {
-    static std::atomic<int> done[4][kMaxDevices];
-    const int kind = (a.is_bf16 ? 2 : 0) + (a.G > 4 ? 1 : 0);
-    auto kern = kind == 3 ? k_quant_attend<true, true> : kind == 2 ? k_quant_attend<true, false>
-              : kind == 1 ? k_quant_attend<false, true> : k_quant_attend<false, false>;
+    static std::atomic<int> done[2][kMaxDevices];
+    const int kind = a.G > 4;
+    auto kern = kind ? k_quant_attend<true> : k_quant_attend<false>;
     cudaError_t e = dyn_smem_limit(kern, (int)sizeof(QaSmem), done[kind]);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(a.workers), dim3(kQaThreads), sizeof(QaSmem), s, a);
     if (e != cudaSuccess) return e;
