@@ -26,6 +26,8 @@ struct QaSmem {
     float4 vs[kQaWarps][kQKeys];         // ... and V
     float size[kQaWarps][kQKeys];        // exponent of each key's largest V scale
     float m[kQaWarps][8], l[kQaWarps][8];
+    uint32_t q[2][kMaxGroup][4][4][8];   // [segment parity][head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
+    float qscale[2][kMaxGroup];
     uint32_t ws[kQaWarps + 1];
     uint32_t pair, first;
     int has[kQaWarps];
@@ -171,6 +173,38 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return fma_half2(w & 
 constexpr float kQaLag = 1.0f;
 constexpr float kQaLift = 13.0f;
 
+// q of one head as 32-bit fixed point of its largest magnitude, in signed
+// bytes, by one warp: lane l has channels 4l .. 4l + 3.
+__device__ __forceinline__ void stage_q(const float v[4], float scale2, uint32_t (*q)[4][8], float *qscale, int lane)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = __reduce_max_sync(kFull, top);
+    // q 2^(156 - e) is below 2^30; a product is 16 (code - 8) times a digit of weight 2^24.  A query with an infinity
+    // or NaN has NaN logits
+    const uint32_t e = min(max(top >> 23, 30u), 254u);
+    const float up = __uint_as_float((283u - e) << 23);
+    if (lane == 0) *qscale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : scale2 * __uint_as_float((e - 9u) << 23);
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++)          // bytes 3, 2, 1, 0: digits 0, 1, 2, 3
+        d[i] = ((uint32_t)__float2int_rn(v[i] * up) + 0x00808080u) ^ 0x00808080u;
+    const int r = lane >> 3, t = (lane & 7) >> 1;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+            reinterpret_cast<uint16_t *>(&q[k][r][2 * t + h])[lane & 1] =
+                (uint16_t)__byte_perm(d[h], d[h + 2], (uint32_t)(3 - k) | (uint32_t)(7 - k) << 4);
+}
+
+__device__ __forceinline__ void load_q(float v[4], const QuantAttendArgs &a, int p, int head, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = ld_as_f32(a.q, ((int64_t)p * a.G + head) * kD + 4 * lane + i, a.is_bf16);
+}
+
 // Attention over a worker's blocks.
 //
 // A warp takes whole blocks of 32 keys from its own ring of bulk copies.
@@ -247,59 +281,33 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     const float high_digit = WIDE || g < 4 ? 1.0f : 0x1p-8f, low_digit = WIDE ? 0x1p-8f : high_digit * 0x1p-16f;
     const float start = -12582912.0f * (high_digit + low_digit + (WIDE ? 0x1p-16f : 0.0f));
 
-    for (uint32_t nb; first < end; first += nb, p++) {
-        nb = block_count(a.c, p);
-        const uint32_t stop = min(end, first + nb);
-        if (nb == 0 || first + nb <= x0) continue;
+    float qv[4];
+    if (warp < G) {
+        load_q(qv, a, p, warp, lane);
+        stage_q(qv, a.scale2, sm.q[0][warp], &sm.qscale[0][warp], lane);
+    }
+    __syncthreads();
+    int turn = 0;
+    while (first < end) {                // segments: pairs that have keys
         const int n = quant_len(a.c, p);
+        const uint32_t nb = (uint32_t)(n + kQKeys - 1) / kQKeys, stop = min(end, first + nb);
         const bool has = x < stop;
         float2 o[4][4];                  // channels 32r + {0, 16, 8, 24} + g, heads 2t and 2t + 1
         float m = -INFINITY;
         float2 l2 = make_float2(0.0f, 0.0f);
         int free_slot = -1;
         if (has) {
-            // q of the head as 32-bit fixed point of its largest magnitude, in signed bytes: digit k of channels
-            // 32r + 8t + {0, 2, 4, 6} and {1, 3, 5, 7}.  A product's rows g and g + 8 hold digits 0 and 1, and 2 (WIDE), or
-            // g / 4 and g / 4 + 2
+            // a product's rows g and g + 8 hold q's digits 0 and 1, and 2 (WIDE), or g / 4 and g / 4 + 2
             uint32_t qd[4][WIDE ? 6 : 4];
-            float qscale;
-            {
-                float v[4][8];
-                uint32_t top = 0;
-                const int64_t base = ((int64_t)p * G + head) * kD + 8 * t;
+            const float qscale = head < G ? sm.qscale[turn][head] : 0.0f;
 #pragma unroll
-                for (int r = 0; r < 4; r++)
+            for (int r = 0; r < 4; r++)
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        v[r][i] = head < G ? ld_as_f32(a.q, base + 32 * r + i, a.is_bf16) : 0.0f;
-                        top = max(top, __float_as_uint(v[r][i]) & 0x7fffffffu);
-                    }
-                top = max(top, __shfl_xor_sync(kFull, top, 1));
-                top = max(top, __shfl_xor_sync(kFull, top, 2));
-                // q 2^(156 - e) is below 2^30; a product is 16 (code - 8) times a digit of weight 2^24.  A query with an
-                // infinity or NaN has NaN logits
-                const uint32_t e = min(max(top >> 23, 30u), 254u);
-                const float up = __uint_as_float((283u - e) << 23);
-                qscale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a.scale2 * __uint_as_float((e - 9u) << 23);
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    uint32_t d[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++)      // bytes 3, 2, 1, 0: digits 0, 1, 2, 3
-                        d[i] = ((uint32_t)__float2int_rn(v[r][i] * up) + 0x00808080u) ^ 0x00808080u;
-                    const int first = WIDE ? 3 : 3 - (g >> 2), second = WIDE ? 2 : 1 - (g >> 2);
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        auto digit = [&](int k) {
-                            const uint32_t s = (uint32_t)k | (uint32_t)(k + 4) << 4;
-                            return __byte_perm(__byte_perm(d[h], d[h + 2], s), __byte_perm(d[h + 4], d[h + 6], s), 0x5410);
-                        };
-                        qd[r][2 * h] = digit(first);
-                        qd[r][2 * h + 1] = digit(second);
-                        if (WIDE) qd[r][4 + h] = digit(1);
-                    }
+                for (int k = 0; k < (WIDE ? 3 : 2); k++) {
+                    const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[turn][head][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
+                    qd[r][k < 2 ? k : 4] = head < G ? d.x : 0u;
+                    qd[r][k < 2 ? k + 2 : 5] = head < G ? d.y : 0u;
                 }
-            }
 #pragma unroll
             for (int r = 0; r < 4; r++)
 #pragma unroll
@@ -463,6 +471,11 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             }
         }
         if (lane == 0) sm.has[warp] = has ? free_slot : -1;
+        int next = p + 1;                // the next segment's pair, and its q
+        if (stop < end) {
+            while (block_count(a.c, next) == 0) next++;
+            if (warp < G) load_q(qv, a, next, warp, lane);
+        }
         __syncthreads();
         float *part = a.part + (int64_t)(p + blockIdx.x) * G * kQPart;
         for (int e = tid; e < G * kD; e += kQaThreads) {
@@ -487,8 +500,12 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
                 part[h * kQPart + kD + 1] = ls;
             }
         }
+        turn ^= 1;
+        if (stop < end && warp < G) stage_q(qv, a.scale2, sm.q[turn][warp], &sm.qscale[turn][warp], lane);
         __syncthreads();
         if (free_slot >= 0) fetch(free_slot);
+        first += nb;
+        p = next;
     }
     if (late && lane == 0 && a.c.status && atomicCAS(a.c.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.c.status[1] = p;
 }
