@@ -16,6 +16,7 @@ from ._lib import (KERNELS, PK_BF16, PK_F32, PK_KV_DEVICE, PK_KV_HOST_PINNED, PK
                    PK_QUANT_KEYS, pk_debug_out, pk_info, pk_params, pk_quant_cache)
 
 _handle = None
+_raw_stream = []                         # torch's raw stream getter, once CUDA is initialised
 
 
 def _L():
@@ -68,7 +69,13 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream:                  # torch.cuda.current_stream() makes an object: 3 us a call
+            return _raw_stream[0](torch.cuda.current_device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = torch.cuda.current_stream()     # initialises CUDA
+        if raw is not None:
+            _raw_stream.append(raw)
+        return stream.cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -9,8 +9,8 @@
 
 namespace pk {
 
-constexpr int kQrThreads = 256;
-constexpr int kQrRows = 64;              // rows (K and V) per CTA
+constexpr int kQrWarps = 8;
+constexpr int kQrThreads = 32 * kQrWarps;
 
 // Code 0..15 of x for a group scale s > 0 with inv = 1 / s (both scaled out of
 // the subnormal range by the caller).  rintf(x inv) can only be wrong next to
@@ -40,58 +40,141 @@ __device__ __forceinline__ float max_mag(float a, float b)
     return (b != b || b > a) ? b : a;
 }
 
+// 8 consecutive elements i .. i + 7 of a bf16 or fp32 array
+__device__ __forceinline__ void load8(float x[8], const void *p, int64_t i, int is_bf16, int vec)
+{
+    if (!vec) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[e] = ld_as_f32(p, i + e, is_bf16);
+    } else if (is_bf16) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + i));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    } else {
+        const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+        const float4 u = __ldcs(f), v = __ldcs(f + 1);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    }
+}
+
+// The word of codes of 8 channels of a group (nibble e: x[e]) and the group's
+// scale bits; the 4 lanes of a group are neighbours.
+__device__ __forceinline__ uint32_t quant_word(const float x[8], uint32_t *scale_bits)
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) m = max_mag(m, fabsf(x[e]));
+    m = max_mag(m, __shfl_xor_sync(kFull, m, 1));
+    m = max_mag(m, __shfl_xor_sync(kFull, m, 2));
+    const uint32_t sb = quant_scale_bits(m);
+    *scale_bits = sb;
+    const float s = bf16_bits_f32(sb);
+    if (!(s > 0.0f)) return 0x88888888u;
+    if (s >= 1e-18f) {
+        // x inv + 1.5 2^23 + 8 rounds to the code in the low bits; codes are joined by adding those bits, shifted, and
+        // taking the constant parts off.  |x| < 7.02 s, so no clamp; a value within rounding of a border is seen by
+        // its remainder and goes the exact way.
+        const float inv = __frcp_rn(s);
+        constexpr float kMagic = 12582920.0f;
+        uint32_t word = 0, base = 0;
+        float far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const float y = fmaf(x[e], inv, kMagic);
+            far = fmaxf(far, fabsf(fmaf(-(y - kMagic), s, x[e])));
+            word += __float_as_uint(y) << (4 * e);
+            base += 0x4b400000u << (4 * e);
+        }
+        if (2.0f * far < s) return word - base;
+    }
+    const float up = s < 1e-18f ? 18446744073709551616.0f : 1.0f;     // 2^64: 1 / s stays finite
+    const float inv = __fdiv_rn(1.0f, s * up);
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) word |= quant_code(x[e] * up, s * up, inv) << (4 * e);
+    return word;
+}
+
+// Transpose of the 4 x 4 bytes of 4 neighbouring lanes' words: lane i gets
+// byte i of lanes 0..3.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane)
+{
+    uint32_t o = __shfl_xor_sync(kFull, w, 1);
+    w = (lane & 1) ? __byte_perm(o, w, 0x7351) : __byte_perm(w, o, 0x6240);   // lanes 2i, 2i + 1: bytes (0, 0', 2, 2') and (1, 1', 3, 3')
+    o = __shfl_xor_sync(kFull, w, 2);
+    return (lane & 2) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+}
+
+// nibbles 0, 2, 4, 6 of a word of bytes 0x0n, and back
+__device__ __forceinline__ uint32_t join_nibbles(uint32_t x)
+{
+    x = (x | x >> 4) & 0x00ff00ffu;
+    return (x | x >> 8) & 0xffffu;
+}
+__device__ __forceinline__ uint32_t spread_nibbles(uint32_t x)
+{
+    x = (x | x << 8) & 0x00ff00ffu;
+    return (x | x << 4) & 0x0f0f0f0fu;
+}
+
+// One warp per 32-key block of the cache.  Two rows at a time, lane (row,
+// group r, quarter t) has channels 32r + 8t .. + 7: its codes are word (t, r)
+// of a K row; of a V row they are nibble t of the 8 chunks, which the 4 lanes
+// of a group exchange.  The block is put together in shared memory and leaves
+// by 16-byte stores.
 __global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a)
 {
+    __shared__ __align__(16) uint8_t s_blk[kQrWarps][kQBlock];
     const int p = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : a.c.lens[p];
     const bool fits = at >= 0 && at + a.n_rows <= a.c.n_cap;
-    if (fits) {
-        const int64_t r0 = (int64_t)blockIdx.x * kQrRows;
-        uint8_t *pair = a.c.blocks + (int64_t)p * (a.c.n_cap / kQKeys) * kQBlock;
-        // one warp per row; lane (r, g) = (lane / 8, lane % 8) of group r
-        const int r = lane >> 3, g = lane & 7;
-        for (int it = warp; it < 2 * kQrRows; it += kQrThreads / 32) {
-            const int64_t i = r0 + (it >> 1);
-            const bool is_v = it & 1;
-            if (i >= a.n_rows) break;
-            const int64_t slot = at + i;
-            const int j = (int)(slot % kQKeys);
-            uint8_t *blk = pair + slot / kQKeys * kQBlock;
-            const void *src = is_v ? a.v : a.k;
-            const int64_t base = ((int64_t)p * a.stride + i) * kD + 32 * r;
-            // K: channels 4g .. 4g + 3 of the group; V: g, g + 8, g + 16, g + 24
-            float x[4];
+    const int64_t b = (fits ? at / kQKeys : 0) + (int64_t)blockIdx.x * kQrWarps + warp;
+    const int64_t i0 = b * kQKeys - at;          // row of the block's first key
+    if (fits && i0 < a.n_rows) {
+        const int j0 = (int)max((int64_t)0, -i0), j1 = (int)min((int64_t)kQKeys, a.n_rows - i0);
+        uint8_t *img = s_blk[warp];
+        const int r = (lane & 15) >> 2, t = lane & 3;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; kv++) {
+            const void *src = kv ? a.v : a.k;
+            const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
+#pragma unroll 4
+            for (int j = (j0 & ~1) + (lane >> 4); j < ((j1 + 1) & ~1); j += 2) {
+                float x[8];
+                if (j >= j0 && j < j1) {
+                    load8(x, src, base + (int64_t)j * kD, a.is_bf16, a.vec);
+                } else {
 #pragma unroll
-            for (int e = 0; e < 4; e++) x[e] = ld_as_f32(src, base + (is_v ? g + 8 * e : 4 * g + e), a.is_bf16);
-            float m = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; e++) m = max_mag(m, fabsf(x[e]));
-#pragma unroll
-            for (int h = 1; h <= 4; h <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, h));
-            const uint32_t sb = quant_scale_bits(m);
-            float s = bf16_bits_f32(sb);
-            uint32_t code = 0x8888u;
-            if (s > 0.0f) {
-                float up = 1.0f;
-                if (s < 1e-18f) up = 18446744073709551616.0f;    // 2^64: 1 / s stays finite
-                s *= up;
-                const float inv = __fdiv_rn(1.0f, s);
-                code = 0;
-#pragma unroll
-                for (int e = 0; e < 4; e++) code |= quant_code(x[e] * up, s, inv) << (4 * e);
-            }
-            if (is_v) {
-                *reinterpret_cast<uint16_t *>(blk + kQOffV + j * kQRow + 8 * (g ^ v_turn(j)) + 2 * r) = (uint16_t)code;
-                if (g == 0) *reinterpret_cast<uint16_t *>(blk + kQOffVs + 8 * j + 2 * r) = (uint16_t)sb;
-            } else {
-                *reinterpret_cast<uint16_t *>(blk + j * kQRow + 16 * (g >> 1) + 4 * r + 2 * (g & 1)) = (uint16_t)code;
-                if (g == 0) *reinterpret_cast<uint16_t *>(blk + kQOffKs + 8 * j + 2 * r) = (uint16_t)sb;
+                    for (int e = 0; e < 8; e++) x[e] = 0.0f;
+                }
+                uint32_t sb, w = quant_word(x, &sb);
+                if (kv) {
+                    w = transpose_bytes(w, lane);      // byte i: channels 8i + 2t, + 1 of the group
+                    uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
+                    *reinterpret_cast<uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j))) = (uint16_t)join_nibbles(w & 0x0f0f0f0fu);
+                    *reinterpret_cast<uint16_t *>(row + 8 * ((2 * t + 1) ^ v_turn(j))) = (uint16_t)join_nibbles(w >> 4 & 0x0f0f0f0fu);
+                } else {
+                    *reinterpret_cast<uint32_t *>(img + j * kQRow + 16 * t + 4 * r) = w;
+                }
+                if (t == 0) *reinterpret_cast<uint16_t *>(img + (kv ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
             }
         }
-        if (a.c.acc)
-            for (int i = threadIdx.x; i < kQrRows && r0 + i < a.n_rows; i += kQrThreads)
-                a.c.acc[(int64_t)p * a.c.n_cap + at + r0 + i] = 0.0f;
+        __syncwarp();
+        uint8_t *dst = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
+        for (int o = 4 * j0 + lane; o < 4 * j1; o += 32) {
+            reinterpret_cast<uint4 *>(dst)[o] = reinterpret_cast<const uint4 *>(img)[o];
+            reinterpret_cast<uint4 *>(dst + kQOffV)[o] = reinterpret_cast<const uint4 *>(img + kQOffV)[o];
+        }
+        if (lane >= j0 && lane < j1) {
+            reinterpret_cast<uint2 *>(dst + kQOffKs)[lane] = reinterpret_cast<const uint2 *>(img + kQOffKs)[lane];
+            reinterpret_cast<uint2 *>(dst + kQOffVs)[lane] = reinterpret_cast<const uint2 *>(img + kQOffVs)[lane];
+            if (a.c.acc) a.c.acc[(int64_t)p * a.c.n_cap + b * kQKeys + lane] = 0.0f;
+        }
     }
     if (gridDim.x == 1) {                // every thread has read lens: the length may change
         __syncthreads();
@@ -113,42 +196,95 @@ __global__ void k_quant_lens(QuantRowsArgs a)
     else quant_devchk(a.c.status, p);
 }
 
+__device__ __forceinline__ void store8(void *p, int64_t i, const float x[8], int is_bf16, int vec)
+{
+    if (is_bf16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        __nv_bfloat16 *d = reinterpret_cast<__nv_bfloat16 *>(p) + i;
+        if (vec) {
+            __stcs(reinterpret_cast<uint4 *>(d), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) reinterpret_cast<uint16_t *>(d)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+    } else {
+        float *d = reinterpret_cast<float *>(p) + i;
+        if (vec) {
+            __stcs(reinterpret_cast<float4 *>(d), make_float4(x[0], x[1], x[2], x[3]));
+            __stcs(reinterpret_cast<float4 *>(d) + 1, make_float4(x[4], x[5], x[6], x[7]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) d[e] = x[e];
+        }
+    }
+}
+
+// Append the other way round: one warp per block.
 __global__ void __launch_bounds__(kQrThreads) k_quant_rows(QuantRowsArgs a)
 {
+    __shared__ __align__(16) uint8_t s_blk[kQrWarps][kQBlock];
     const int p = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : 0;
     const int n = quant_len(a.c, p);
     if (blockIdx.x == 0 && threadIdx.x == 0 && quant_len_bad(a.c, p)) quant_devchk(a.c.status, p);
-    const int64_t r0 = (int64_t)blockIdx.x * kQrRows;
-    const uint8_t *pair = a.c.blocks + (int64_t)p * (a.c.n_cap / kQKeys) * kQBlock;
-    const int r = lane >> 3, g = lane & 7;
-    for (int it = warp; it < 2 * kQrRows; it += kQrThreads / 32) {
-        const int64_t i = r0 + (it >> 1), slot = at + i;
-        if (i >= a.n_rows) break;
-        if (slot < 0 || slot >= n) continue;
-        const bool is_v = it & 1;
-        const int j = (int)(slot % kQKeys);
-        const uint8_t *blk = pair + slot / kQKeys * kQBlock;
-        const uint32_t code = *reinterpret_cast<const uint16_t *>(
-            is_v ? blk + kQOffV + j * kQRow + 8 * (g ^ v_turn(j)) + 2 * r
-                 : blk + j * kQRow + 16 * (g >> 1) + 4 * r + 2 * (g & 1));
-        const float s = bf16_bits_f32(*reinterpret_cast<const uint16_t *>(blk + (is_v ? kQOffVs : kQOffKs) + 8 * j + 2 * r));
-        void *dst = const_cast<void *>(is_v ? a.v : a.k);
-        const int64_t base = ((int64_t)p * a.stride + i) * kD + 32 * r;
+    const int64_t b = max(at, (int64_t)0) / kQKeys + (int64_t)blockIdx.x * kQrWarps + warp;
+    const int64_t i0 = b * kQKeys - at;          // row of the block's first key
+    const int j0 = (int)max((int64_t)0, -i0);
+    const int j1 = (int)max((int64_t)0, min(min((int64_t)kQKeys, a.n_rows - i0), n - b * kQKeys));
+    if (j0 >= j1) return;
+    uint8_t *img = s_blk[warp];
+    const uint8_t *src = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
+    for (int o = 4 * j0 + lane; o < 4 * j1; o += 32) {
+        reinterpret_cast<uint4 *>(img)[o] = __ldcs(reinterpret_cast<const uint4 *>(src) + o);
+        reinterpret_cast<uint4 *>(img + kQOffV)[o] = __ldcs(reinterpret_cast<const uint4 *>(src + kQOffV) + o);
+    }
+    if (lane >= j0 && lane < j1) {
+        reinterpret_cast<uint2 *>(img + kQOffKs)[lane] = reinterpret_cast<const uint2 *>(src + kQOffKs)[lane];
+        reinterpret_cast<uint2 *>(img + kQOffVs)[lane] = reinterpret_cast<const uint2 *>(src + kQOffVs)[lane];
+    }
+    __syncwarp();
+    const int r = (lane & 15) >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; kv++) {
+        void *dst = const_cast<void *>(kv ? a.v : a.k);
+        const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
+#pragma unroll 4
+        for (int j = (j0 & ~1) + (lane >> 4); j < ((j1 + 1) & ~1); j += 2) {
+            uint32_t w;
+            if (kv) {
+                const uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
+                const uint32_t e = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j)));
+                const uint32_t o = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t + 1) ^ v_turn(j)));
+                w = transpose_bytes(spread_nibbles(e) | spread_nibbles(o) << 4, lane);
+            } else {
+                w = *reinterpret_cast<const uint32_t *>(img + j * kQRow + 16 * t + 4 * r);
+            }
+            if (j < j0 || j >= j1) continue;
+            const float s = bf16_bits_f32(*reinterpret_cast<const uint16_t *>(img + (kv ? kQOffVs : kQOffKs) + 8 * j + 2 * r));
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float x = (float)((int)((code >> (4 * e)) & 15u) - 8) * s;
-            const int64_t o = base + (is_v ? g + 8 * e : 4 * g + e);
-            if (a.is_bf16) reinterpret_cast<__nv_bfloat16 *>(dst)[o] = __float2bfloat16_rn(x);
-            else reinterpret_cast<float *>(dst)[o] = x;
+            for (int e = 0; e < 8; e++) x[e] = ((float)((w >> (4 * e)) & 15u) - 8.0f) * s;
+            store8(dst, base + (int64_t)j * kD, x, a.is_bf16, a.vec);
         }
     }
 }
 
+// CTAs per pair: the blocks that n rows can touch, from any place on
+static unsigned row_tiles(int64_t n)
+{
+    const int64_t blocks = (n + 2 * kQKeys - 2) / kQKeys;
+    return (unsigned)((blocks + kQrWarps - 1) / kQrWarps);
+}
+
 cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s)
 {
-    const unsigned tiles = (unsigned)((a.n_rows + kQrRows - 1) / kQrRows);
+    const unsigned tiles = row_tiles(a.n_rows);
     cudaError_t e = launch_pdl(k_quant_append, dim3(tiles, a.c.bh), dim3(kQrThreads), 0, s, a);
     if (e == cudaSuccess && tiles > 1)
         e = launch_pdl(k_quant_lens, dim3((a.c.bh + 255) / 256), dim3(256), 0, s, a);
@@ -157,8 +293,7 @@ cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s)
 
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t s)
 {
-    const unsigned tiles = (unsigned)((a.n_rows + kQrRows - 1) / kQrRows);
-    return launch_pdl(k_quant_rows, dim3(tiles, a.c.bh), dim3(kQrThreads), 0, s, a);
+    return launch_pdl(k_quant_rows, dim3(row_tiles(a.n_rows), a.c.bh), dim3(kQrThreads), 0, s, a);
 }
 
 }  // namespace pk
