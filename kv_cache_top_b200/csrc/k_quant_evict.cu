@@ -5,11 +5,11 @@
 // CTA a run of its slots: a radix select over the ordered bits of acc (three
 // digits, the CTAs' histograms joined through distributed shared memory)
 // gives the threshold weight, the CTAs' counts of kept keys and ties their
-// places, and each CTA moves its own kept rows.
+// places, and each CTA lists its kept slots and moves their rows.
 //
-// Memory bounds it where rows are long: acc is read once from HBM and three
-// more times from L2, kept rows are read and written once.  The order of the
-// rows is kept, so the result does not depend on the split.
+// A run of up to kQeTile slots is read from HBM once and stays in shared
+// memory; a longer one is read again for each digit.  The order of the rows is
+// kept, so the result does not depend on the split.
 #include <cooperative_groups.h>
 
 #include "pk_launch.cuh"
@@ -22,15 +22,17 @@ namespace pk {
 constexpr int kQeThreads = 512;
 constexpr int kQeWarps = kQeThreads / 32;
 constexpr int kQeBins = 2048;            // 11, 11 and 10 bits
-constexpr int kQeChunk = 4 * kQeThreads; // slots a CTA looks at in one step
+constexpr int kQeTile = 16384;           // slots in shared memory: two CTAs to an SM
 constexpr int kQeMaxCluster = 8;
 
 struct QeSmem {
+    uint32_t key[kQeTile];
+    uint16_t list[kQeTile];              // kept slots of the tile, from its first on
     uint32_t hist[2][kQeBins];           // of the digit in turn: while the CTAs still read one, the next counts
     uint32_t ws[kQeWarps + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
-    int list[kQeChunk];
+    uint32_t kept[kQeWarps], ties[kQeWarps];
 };
 
 // ordered bits of a weight; NaN sorts below everything
@@ -39,21 +41,23 @@ __device__ __forceinline__ uint32_t weight_key(float x)
     return x != x ? 0u : ord_f32(x + 0.0f);
 }
 
-// slots 4 at a time: the CTA's thread t has slots at + 4t .. + 3 (outside [lo, hi): 0 and not counted)
-__device__ __forceinline__ void load_keys(uint32_t k[4], const float *acc, int64_t i, int64_t hi, bool vec)
+// keys of slots [i0, i0 + count) to shared memory
+__device__ __forceinline__ void load_tile(uint32_t *key, const float *acc, int64_t i0, int count, bool vec)
 {
-    if (vec && i + 4 <= hi) {
-        const float4 v = *reinterpret_cast<const float4 *>(acc + i);
-        k[0] = weight_key(v.x), k[1] = weight_key(v.y), k[2] = weight_key(v.z), k[3] = weight_key(v.w);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; e++) k[e] = i + e < hi ? weight_key(acc[i + e]) : 0u;
+    acc += i0;
+    if (vec) {
+#pragma unroll 4
+        for (int i = 4 * threadIdx.x; i + 4 <= count; i += 4 * kQeThreads) {
+            const float4 v = *reinterpret_cast<const float4 *>(acc + i);
+            *reinterpret_cast<uint4 *>(key + i) = make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
+        }
     }
+    for (int i = (vec ? count / 4 * 4 : 0) + threadIdx.x; i < count; i += kQeThreads) key[i] = weight_key(acc[i]);
 }
 
-// Rows src[list[j]] to slots o0 + j, j < count (pair bases), by the CTA's
+// Rows i0 + list[j] of src to slots o0 + j of dst, j < count, by the CTA's
 // warps: 32 rows at a time, 16 bytes a lane.
-__device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, const int *list, int count, int64_t o0)
+__device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, int64_t i0, const uint16_t *list, int count, int64_t o0)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint8_t *src = a.src.blocks + (int64_t)p * (a.src.n_cap / kQKeys) * kQBlock;
@@ -69,7 +73,7 @@ __device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, const 
         for (int i = 0; i < 4; i++) {        // rows 8i + lane / 4, quarter lane % 4
             const int j = 8 * i + (lane >> 2);
             if (j < m) {
-                const int x = list[j0 + j];
+                const int x = (int)i0 + list[j0 + j];
                 const uint8_t *b = src + (int64_t)(x / kQKeys) * kQBlock + x % kQKeys * kQRow;
                 kc[i] = __ldcs(reinterpret_cast<const uint4 *>(b) + (lane & 3));
                 // chunk places of V differ by the turn of the slot: taken in the order of slots with no turn
@@ -77,7 +81,7 @@ __device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, const 
             }
         }
         if (lane < m) {
-            slot = list[j0 + lane];
+            slot = (int)i0 + list[j0 + lane];
             const uint8_t *b = src + (int64_t)(slot / kQKeys) * kQBlock;
             ks = *reinterpret_cast<const uint2 *>(b + kQOffKs + 8 * (slot % kQKeys));
             vs = *reinterpret_cast<const uint2 *>(b + kQOffVs + 8 * (slot % kQKeys));
@@ -107,9 +111,11 @@ __device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, const 
 
 __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
 {
-    __shared__ QeSmem sm;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    QeSmem &sm = *reinterpret_cast<QeSmem *>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
-    const int p = blockIdx.y, tid = threadIdx.x, rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     pdl_wait();
     const int n = quant_len(a.src, p);
     if (rank == 0 && tid == 0 && quant_len_bad(a.src, p)) quant_devchk(a.src.status, p);
@@ -121,39 +127,54 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     // this CTA's slots [c0, c1)
     const int64_t run = ((n + ranks - 1) / ranks + 3) / 4 * 4;
     const int64_t c0 = min((int64_t)n, rank * run), c1 = min((int64_t)n, c0 + run);
-    auto contested = [&](int64_t i) { return i >= lo && i < hi; };
+    int64_t held = -1;                               // first slot of the tile in shared memory
+    auto tile = [&](int64_t c) {
+        if (held == c || !need) return;
+        __syncthreads();
+        load_tile(sm.key, acc, c, (int)min((int64_t)kQeTile, c1 - c), vec);
+        held = c;
+        __syncthreads();
+    };
 
     // threshold key: the need-th largest of the contested; left: how many of those equal to it stay
     uint32_t prefix = 0, left = need;
     if (need) {
-#pragma unroll
+#pragma unroll 1
         for (int d = 0; d < 3; d++) {
             const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
             const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffffc00u;
             uint32_t *hist = sm.hist[d & 1];
             for (int i = tid; i < bins; i += kQeThreads) hist[i] = 0;
             __syncthreads();
-            for (int64_t c = c0; c < c1; c += kQeChunk) {
-                const int64_t i = c + 4 * tid;
-                uint32_t k[4];
-                load_keys(k, acc, i, c1, vec);
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (i + e < c1 && contested(i + e) && (k[e] & above) == prefix) atomicAdd(&hist[(k[e] >> shift) & (bins - 1)], 1u);
+            for (int64_t c = c0; c < c1; c += kQeTile) {
+                tile(c);
+                const int first = (int)max((int64_t)0, lo - c), end = (int)min(min((int64_t)kQeTile, c1 - c), hi - c);
+#pragma unroll 4
+                for (int i = first + tid; i < end; i += kQeThreads) {
+                    const uint32_t k = sm.key[i];
+                    if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+                }
             }
             cluster.sync();
             // all CTAs' counts; thread t has bins [per t, per (t + 1))
             const int per = bins / kQeThreads;
-            uint32_t mine[4], total = 0;
-            for (int e = 0; e < per; e++) {
-                mine[e] = 0;
-                for (int w = 0; w < ranks; w++) mine[e] += cluster.map_shared_rank(hist, w)[per * tid + e];
-                total += mine[e];
+            uint32_t mine[4] = {0, 0, 0, 0}, total = 0;
+            for (int w = 0; w < ranks; w++) {
+                const uint32_t *h = cluster.map_shared_rank(hist, w) + per * tid;
+                if (per == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(h);
+                    mine[0] += v.x, mine[1] += v.y, mine[2] += v.z, mine[3] += v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(h);
+                    mine[0] += v.x, mine[1] += v.y;
+                }
             }
+            total = mine[0] + mine[1] + mine[2] + mine[3];
             uint32_t sum;
             uint32_t over = block_excl_scan<kQeThreads>(total, sm.ws, &sum);
             over = sum - over - total;               // keys in the bins above the thread's
-            for (int e = per - 1; e >= 0; e--) {
+#pragma unroll
+            for (int e = 3; e >= 0; e--) {
                 if (over < left && over + mine[e] >= left) {
                     sm.digit = per * tid + e;
                     sm.left = left - over;
@@ -166,27 +187,45 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
             __syncthreads();
         }
     }
+    // a warp's share of a tile: whole groups of 32 slots; what its lane's slot is: 2 kept, 1 tied, 0 dropped
+    auto kind = [&](int64_t c, int i) {
+        const int64_t s = c + i;
+        if (s >= c1) return 0;
+        if (s < lo || s >= hi) return 2;
+        if (!need) return 0;
+        const uint32_t k = sm.key[i];
+        return k > prefix ? 2 : k == prefix ? 1 : 0;
+    };
+    constexpr int kShare = kQeTile / kQeWarps;
+    auto count = [&](int64_t c, uint32_t *kept, uint32_t *ties) {
+        // shares of ceil(slots / warps) rounded up to groups
+        const int m = (int)min((int64_t)kQeTile, c1 - c), share = ((m + kQeWarps - 1) / kQeWarps + 31) / 32 * 32;
+        uint32_t x = 0, y = 0;
+        for (int i = warp * share; i < min(m, (warp + 1) * share); i += 32) {
+            const int k = kind(c, i + lane);
+            x += __popc(__ballot_sync(kFull, k == 2));
+            y += __popc(__ballot_sync(kFull, k == 1));
+        }
+        *kept = x;
+        *ties = y;
+        return share;
+    };
+    static_assert(kShare % 32 == 0, "shares are whole groups");
+
     // kept and tied slots of this CTA, and of those before it
     uint32_t before = 0, ties_before = 0;
     {
         uint32_t kept = 0, ties = 0;
-        for (int64_t c = c0; c < c1; c += kQeChunk) {
-            const int64_t i = c + 4 * tid;
-            uint32_t k[4];
-            if (need) load_keys(k, acc, i, c1, vec);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                if (i + e >= c1) continue;
-                if (!contested(i + e)) kept++;
-                else if (need && k[e] > prefix) kept++;
-                else if (need && k[e] == prefix) ties++;
-            }
+        for (int64_t c = c0; c < c1; c += kQeTile) {
+            uint32_t x, y;
+            tile(c);
+            count(c, &x, &y);
+            kept += x;
+            ties += y;
         }
-        kept = __reduce_add_sync(kFull, kept);
-        ties = __reduce_add_sync(kFull, ties);
         if (tid < 2) sm.count[tid] = 0;
         __syncthreads();
-        if ((tid & 31) == 0) {
+        if (lane == 0) {
             atomicAdd(&sm.count[0], kept);
             atomicAdd(&sm.count[1], ties);
         }
@@ -198,34 +237,35 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         }
         before += min(ties_before, left);            // ties that stay are the lowest
     }
-    for (int64_t c = c0; c < c1; c += kQeChunk) {
-        const int64_t i = c + 4 * tid;
-        uint32_t k[4];
-        if (need) load_keys(k, acc, i, c1, vec);
-        uint32_t keep = 0, tie = 0;                  // bit e: slot i + e
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            if (i + e >= c1) continue;
-            if (!contested(i + e) || (need && k[e] > prefix)) keep |= 1u << e;
-            else if (need && k[e] == prefix) tie |= 1u << e;
+    for (int64_t c = c0; c < c1; c += kQeTile) {
+        uint32_t x, y;
+        tile(c);
+        const int share = count(c, &x, &y), m = (int)min((int64_t)kQeTile, c1 - c);
+        if (lane == 0) {
+            sm.kept[warp] = x;
+            sm.ties[warp] = y;
         }
-        uint32_t total;
-        uint32_t rest = block_excl_scan<kQeThreads>(__popc(tie), sm.ws, &total);
-        rest += ties_before;
-        ties_before += total;
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (tie >> e & 1) {
-                if (rest < left) keep |= 1u << e;
-                rest++;
-            }
-        uint32_t at = block_excl_scan<kQeThreads>(__popc(keep), sm.ws, &total);
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (keep >> e & 1) sm.list[at++] = (int)(i + e);
         __syncthreads();
-        move_rows(a, p, sm.list, (int)total, before);
+        uint32_t at = 0, ties = ties_before, total = 0, all_ties = ties_before;   // of the warps before; of all
+        for (int w = 0; w < kQeWarps; w++) {
+            const uint32_t stay = min(all_ties + sm.ties[w], left) - min(all_ties, left);
+            if (w < warp) at += sm.kept[w] + stay, ties += sm.ties[w];
+            total += sm.kept[w] + stay;
+            all_ties += sm.ties[w];
+        }
+        for (int i = warp * share; i < min(m, (warp + 1) * share); i += 32) {
+            const int k = kind(c, i + lane);
+            const uint32_t tied = __ballot_sync(kFull, k == 1), below = (1u << lane) - 1;
+            const bool keep = k == 2 || (k == 1 && ties + __popc(tied & below) < left);
+            const uint32_t kept = __ballot_sync(kFull, keep);
+            if (keep) sm.list[at + __popc(kept & below)] = (uint16_t)(i + lane);
+            at += __popc(kept);
+            ties += __popc(tied);
+        }
+        __syncthreads();
+        move_rows(a, p, c, sm.list, (int)total, before);
         before += total;
+        ties_before = all_ties;
         __syncthreads();
     }
     const int64_t kept = all ? n : a.budget;
@@ -241,12 +281,18 @@ cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // CTAs per pair: about four per SM in all, each with two steps of slots at least
+    static std::atomic<int> done[kMaxDevices];
+    e = dyn_smem_limit(k_quant_evict, (int)sizeof(QeSmem), done);
+    if (e != cudaSuccess) return e;
+    // CTAs per pair: as many as hold its slots in shared memory, and more while there is room for all at once
     int c = 1;
-    while (c < kQeMaxCluster && 2 * c * a.src.bh <= 4 * sms && a.src.n_cap / (2 * c) >= 2 * kQeChunk) c *= 2;
+    while (c < kQeMaxCluster && (a.src.n_cap > (int64_t)c * kQeTile ||
+                                 (2 * c * a.src.bh <= 2 * sms && a.src.n_cap >= 2 * c * 256)))
+        c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c, a.src.bh);
     cfg.blockDim = dim3(kQeThreads);
+    cfg.dynamicSmemBytes = sizeof(QeSmem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

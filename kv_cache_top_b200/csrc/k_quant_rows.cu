@@ -34,43 +34,65 @@ __device__ __forceinline__ uint32_t quant_scale_bits(float m)
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(m, 7.0f)));
 }
 
-// largest magnitude that keeps a NaN (fmaxf would drop it)
-__device__ __forceinline__ float max_mag(float a, float b)
+// 8 consecutive elements i .. i + 7 of a bf16 or fp32 array, as they lie
+struct Raw8 {
+    uint32_t w[8];                       // fp32, or 4 words of 2 bf16
+};
+template <bool BF16>
+__device__ __forceinline__ Raw8 load8(const void *p, int64_t i, int vec)
 {
-    return (b != b || b > a) ? b : a;
-}
-
-// 8 consecutive elements i .. i + 7 of a bf16 or fp32 array
-__device__ __forceinline__ void load8(float x[8], const void *p, int64_t i, int is_bf16, int vec)
-{
-    if (!vec) {
+    Raw8 x;
+    if (BF16) {
+        const __nv_bfloat16 *b = reinterpret_cast<const __nv_bfloat16 *>(p) + i;
+        if (vec) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(b));
+            x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(b);
 #pragma unroll
-        for (int e = 0; e < 8; e++) x[e] = ld_as_f32(p, i + e, is_bf16);
-    } else if (is_bf16) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + i));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            x[2 * e] = __uint_as_float(w[e] << 16);
-            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            for (int e = 0; e < 4; e++) x.w[e] = h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
         }
     } else {
-        const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-        const float4 u = __ldcs(f), v = __ldcs(f + 1);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+        const uint32_t *f = reinterpret_cast<const uint32_t *>(p) + i;
+        if (vec) {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(f)), v = __ldcs(reinterpret_cast<const uint4 *>(f) + 1);
+            x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w, x.w[4] = v.x, x.w[5] = v.y, x.w[6] = v.z, x.w[7] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) x.w[e] = f[e];
+        }
     }
+    return x;
 }
 
 // The word of codes of 8 channels of a group (nibble e: x[e]) and the group's
 // scale bits; the 4 lanes of a group are neighbours.
-__device__ __forceinline__ uint32_t quant_word(const float x[8], uint32_t *scale_bits)
+template <bool BF16>
+__device__ __forceinline__ uint32_t quant_word(const Raw8 &raw, uint32_t *scale_bits)
 {
-    float m = 0.0f;
+    // the largest magnitude, as bits: those of infinities and NaN are larger than all others
+    uint32_t top;
+    float x[8];
+    if (BF16) {
+        top = __vmaxu2(__vmaxu2(raw.w[0] & 0x7fff7fffu, raw.w[1] & 0x7fff7fffu),
+                       __vmaxu2(raw.w[2] & 0x7fff7fffu, raw.w[3] & 0x7fff7fffu));
+        top = max(top & 0xffff0000u, top << 16);
 #pragma unroll
-    for (int e = 0; e < 8; e++) m = max_mag(m, fabsf(x[e]));
-    m = max_mag(m, __shfl_xor_sync(kFull, m, 1));
-    m = max_mag(m, __shfl_xor_sync(kFull, m, 2));
-    const uint32_t sb = quant_scale_bits(m);
+        for (int e = 0; e < 4; e++) {
+            x[2 * e] = __uint_as_float(raw.w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(raw.w[e] & 0xffff0000u);
+        }
+    } else {
+        top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            top = max(top, raw.w[e] & 0x7fffffffu);
+            x[e] = __uint_as_float(raw.w[e]);
+        }
+    }
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    const uint32_t sb = quant_scale_bits(__uint_as_float(top));
     *scale_bits = sb;
     const float s = bf16_bits_f32(sb);
     if (!(s > 0.0f)) return 0x88888888u;
@@ -78,7 +100,8 @@ __device__ __forceinline__ uint32_t quant_word(const float x[8], uint32_t *scale
         // x inv + 1.5 2^23 + 8 rounds to the code in the low bits; codes are joined by adding those bits, shifted, and
         // taking the constant parts off.  |x| < 7.02 s, so no clamp; a value within rounding of a border is seen by
         // its remainder and goes the exact way.
-        const float inv = __frcp_rn(s);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
         constexpr float kMagic = 12582920.0f;
         uint32_t word = 0, base = 0;
         float far = 0.0f;
@@ -121,39 +144,38 @@ __device__ __forceinline__ uint32_t spread_nibbles(uint32_t x)
     return (x | x << 4) & 0x0f0f0f0fu;
 }
 
-// One warp per 32-key block of the cache.  Two rows at a time, lane (row,
-// group r, quarter t) has channels 32r + 8t .. + 7: its codes are word (t, r)
-// of a K row; of a V row they are nibble t of the 8 chunks, which the 4 lanes
-// of a group exchange.  The block is put together in shared memory and leaves
-// by 16-byte stores.
-__global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a)
+// One CTA per 32-key block of the cache (or, of few rows, per pair).  A warp
+// has rows 4w .. 4w + 3, two at a time: lane (row, group r, quarter t) has
+// channels 32r + 8t .. + 7, whose codes are word (t, r) of a K row; of a V row
+// they are nibble t of the 8 chunks, which the 4 lanes of a group exchange.
+// The block is put together in shared memory and leaves by 16-byte stores.
+template <bool BF16>
+__global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a, int tiles)
 {
-    __shared__ __align__(16) uint8_t s_blk[kQrWarps][kQBlock];
-    const int p = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ __align__(16) uint8_t img[kQBlock];
+    const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : a.c.lens[p];
     const bool fits = at >= 0 && at + a.n_rows <= a.c.n_cap;
-    const int64_t b = (fits ? at / kQKeys : 0) + (int64_t)blockIdx.x * kQrWarps + warp;
-    const int64_t i0 = b * kQKeys - at;          // row of the block's first key
-    if (fits && i0 < a.n_rows) {
+    const int r = (lane & 15) >> 2, t = lane & 3;
+    for (int tile = blockIdx.x; fits && tile < tiles; tile += gridDim.x) {
+        const int64_t b = at / kQKeys + tile, i0 = b * kQKeys - at;          // row of the block's first key
+        if (i0 >= a.n_rows) break;
         const int j0 = (int)max((int64_t)0, -i0), j1 = (int)min((int64_t)kQKeys, a.n_rows - i0);
-        uint8_t *img = s_blk[warp];
-        const int r = (lane & 15) >> 2, t = lane & 3;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; kv++) {
-            const void *src = kv ? a.v : a.k;
+        if (4 * warp < j1 && 4 * warp + 4 > j0) {
             const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
-#pragma unroll 4
-            for (int j = (j0 & ~1) + (lane >> 4); j < ((j1 + 1) & ~1); j += 2) {
-                float x[8];
-                if (j >= j0 && j < j1) {
-                    load8(x, src, base + (int64_t)j * kD, a.is_bf16, a.vec);
-                } else {
+            Raw8 x[4];                   // K rows 4w + 2i + lane / 16, then V
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = 0.0f;
-                }
-                uint32_t sb, w = quant_word(x, &sb);
-                if (kv) {
+            for (int i = 0; i < 4; i++) {
+                const int j = 4 * warp + 2 * (i & 1) + (lane >> 4);
+                x[i] = Raw8{};
+                if (j >= j0 && j < j1) x[i] = load8<BF16>(i >> 1 ? a.v : a.k, base + (int64_t)j * kD, a.vec);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int j = 4 * warp + 2 * (i & 1) + (lane >> 4);
+                uint32_t sb, w = quant_word<BF16>(x[i], &sb);
+                if (i >> 1) {
                     w = transpose_bytes(w, lane);      // byte i: channels 8i + 2t, + 1 of the group
                     uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
                     *reinterpret_cast<uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j))) = (uint16_t)join_nibbles(w & 0x0f0f0f0fu);
@@ -161,24 +183,21 @@ __global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a)
                 } else {
                     *reinterpret_cast<uint32_t *>(img + j * kQRow + 16 * t + 4 * r) = w;
                 }
-                if (t == 0) *reinterpret_cast<uint16_t *>(img + (kv ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
+                if (t == 0) *reinterpret_cast<uint16_t *>(img + (i >> 1 ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
             }
         }
-        __syncwarp();
+        __syncthreads();
         uint8_t *dst = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
-        for (int o = 4 * j0 + lane; o < 4 * j1; o += 32) {
-            reinterpret_cast<uint4 *>(dst)[o] = reinterpret_cast<const uint4 *>(img)[o];
-            reinterpret_cast<uint4 *>(dst + kQOffV)[o] = reinterpret_cast<const uint4 *>(img + kQOffV)[o];
-        }
-        if (lane >= j0 && lane < j1) {
-            reinterpret_cast<uint2 *>(dst + kQOffKs)[lane] = reinterpret_cast<const uint2 *>(img + kQOffKs)[lane];
-            reinterpret_cast<uint2 *>(dst + kQOffVs)[lane] = reinterpret_cast<const uint2 *>(img + kQOffVs)[lane];
-            if (a.c.acc) a.c.acc[(int64_t)p * a.c.n_cap + b * kQKeys + lane] = 0.0f;
-        }
+        const int o = tid & 127, off = tid >> 7 ? kQOffV : 0;
+        if (o >= 4 * j0 && o < 4 * j1) reinterpret_cast<uint4 *>(dst + off)[o] = reinterpret_cast<const uint4 *>(img + off)[o];
+        if (tid < 2 * kQKeys && (tid & 31) >= j0 && (tid & 31) < j1)
+            reinterpret_cast<uint2 *>(dst + kQOffKs)[tid] = reinterpret_cast<const uint2 *>(img + kQOffKs)[tid];
+        if (a.c.acc && tid >= j0 && tid < j1) a.c.acc[(int64_t)p * a.c.n_cap + b * kQKeys + tid] = 0.0f;
+        if (gridDim.x < tiles) __syncthreads();
     }
     if (gridDim.x == 1) {                // every thread has read lens: the length may change
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             if (fits) a.c.lens[p] = (int32_t)(at + a.n_rows);
             else quant_devchk(a.c.status, p);
         }
@@ -196,9 +215,10 @@ __global__ void k_quant_lens(QuantRowsArgs a)
     else quant_devchk(a.c.status, p);
 }
 
-__device__ __forceinline__ void store8(void *p, int64_t i, const float x[8], int is_bf16, int vec)
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int64_t i, const float x[8], int vec)
 {
-    if (is_bf16) {
+    if (BF16) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -224,76 +244,64 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float x[8], int
     }
 }
 
-// Append the other way round: one warp per block.
+// Append the other way round: one CTA per block.
+template <bool BF16>
 __global__ void __launch_bounds__(kQrThreads) k_quant_rows(QuantRowsArgs a)
 {
-    __shared__ __align__(16) uint8_t s_blk[kQrWarps][kQBlock];
-    const int p = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ __align__(16) uint8_t img[kQBlock];
+    const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : 0;
     const int n = quant_len(a.c, p);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && quant_len_bad(a.c, p)) quant_devchk(a.c.status, p);
-    const int64_t b = max(at, (int64_t)0) / kQKeys + (int64_t)blockIdx.x * kQrWarps + warp;
+    if (blockIdx.x == 0 && tid == 0 && quant_len_bad(a.c, p)) quant_devchk(a.c.status, p);
+    const int64_t b = max(at, (int64_t)0) / kQKeys + blockIdx.x;
     const int64_t i0 = b * kQKeys - at;          // row of the block's first key
     const int j0 = (int)max((int64_t)0, -i0);
     const int j1 = (int)max((int64_t)0, min(min((int64_t)kQKeys, a.n_rows - i0), n - b * kQKeys));
     if (j0 >= j1) return;
-    uint8_t *img = s_blk[warp];
     const uint8_t *src = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
-    for (int o = 4 * j0 + lane; o < 4 * j1; o += 32) {
-        reinterpret_cast<uint4 *>(img)[o] = __ldcs(reinterpret_cast<const uint4 *>(src) + o);
-        reinterpret_cast<uint4 *>(img + kQOffV)[o] = __ldcs(reinterpret_cast<const uint4 *>(src + kQOffV) + o);
-    }
-    if (lane >= j0 && lane < j1) {
-        reinterpret_cast<uint2 *>(img + kQOffKs)[lane] = reinterpret_cast<const uint2 *>(src + kQOffKs)[lane];
-        reinterpret_cast<uint2 *>(img + kQOffVs)[lane] = reinterpret_cast<const uint2 *>(src + kQOffVs)[lane];
-    }
-    __syncwarp();
+    reinterpret_cast<uint4 *>(img)[tid] = __ldcs(reinterpret_cast<const uint4 *>(src) + tid);
+    if (tid < kQBlock / 16 - kQrThreads) reinterpret_cast<uint4 *>(img)[kQrThreads + tid] = __ldcs(reinterpret_cast<const uint4 *>(src) + kQrThreads + tid);
+    __syncthreads();
     const int r = (lane & 15) >> 2, t = lane & 3;
-#pragma unroll 1
-    for (int kv = 0; kv < 2; kv++) {
-        void *dst = const_cast<void *>(kv ? a.v : a.k);
-        const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
-#pragma unroll 4
-        for (int j = (j0 & ~1) + (lane >> 4); j < ((j1 + 1) & ~1); j += 2) {
-            uint32_t w;
-            if (kv) {
-                const uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
-                const uint32_t e = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j)));
-                const uint32_t o = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t + 1) ^ v_turn(j)));
-                w = transpose_bytes(spread_nibbles(e) | spread_nibbles(o) << 4, lane);
-            } else {
-                w = *reinterpret_cast<const uint32_t *>(img + j * kQRow + 16 * t + 4 * r);
-            }
-            if (j < j0 || j >= j1) continue;
-            const float s = bf16_bits_f32(*reinterpret_cast<const uint16_t *>(img + (kv ? kQOffVs : kQOffKs) + 8 * j + 2 * r));
-            float x[8];
+    const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
 #pragma unroll
-            for (int e = 0; e < 8; e++) x[e] = ((float)((w >> (4 * e)) & 15u) - 8.0f) * s;
-            store8(dst, base + (int64_t)j * kD, x, a.is_bf16, a.vec);
+    for (int i = 0; i < 4; i++) {
+        const int j = 4 * warp + 2 * (i & 1) + (lane >> 4);
+        uint32_t w;
+        if (i >> 1) {
+            const uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
+            const uint32_t e = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j)));
+            const uint32_t o = *reinterpret_cast<const uint16_t *>(row + 8 * ((2 * t + 1) ^ v_turn(j)));
+            w = transpose_bytes(spread_nibbles(e) | spread_nibbles(o) << 4, lane);
+        } else {
+            w = *reinterpret_cast<const uint32_t *>(img + j * kQRow + 16 * t + 4 * r);
         }
+        if (j < j0 || j >= j1) continue;
+        const float s = bf16_bits_f32(*reinterpret_cast<const uint16_t *>(img + (i >> 1 ? kQOffVs : kQOffKs) + 8 * j + 2 * r));
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[e] = ((float)((w >> (4 * e)) & 15u) - 8.0f) * s;
+        store8<BF16>(const_cast<void *>(i >> 1 ? a.v : a.k), base + (int64_t)j * kD, x, a.vec);
     }
 }
 
-// CTAs per pair: the blocks that n rows can touch, from any place on
-static unsigned row_tiles(int64_t n)
-{
-    const int64_t blocks = (n + 2 * kQKeys - 2) / kQKeys;
-    return (unsigned)((blocks + kQrWarps - 1) / kQrWarps);
-}
+// blocks that n rows can touch, from any place on
+static int row_tiles(int64_t n) { return (int)((n + 2 * kQKeys - 2) / kQKeys); }
 
 cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s)
 {
-    const unsigned tiles = row_tiles(a.n_rows);
-    cudaError_t e = launch_pdl(k_quant_append, dim3(tiles, a.c.bh), dim3(kQrThreads), 0, s, a);
-    if (e == cudaSuccess && tiles > 1)
+    // up to 4 blocks a pair: one CTA does them in turn and sets the length; a second launch would cost more
+    const int tiles = row_tiles(a.n_rows), ctas = tiles <= 4 ? 1 : tiles;
+    cudaError_t e = launch_pdl(a.is_bf16 ? k_quant_append<true> : k_quant_append<false>, dim3(ctas, a.c.bh), dim3(kQrThreads), 0, s, a, tiles);
+    if (e == cudaSuccess && ctas > 1)
         e = launch_pdl(k_quant_lens, dim3((a.c.bh + 255) / 256), dim3(256), 0, s, a);
     return e;
 }
 
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t s)
 {
-    return launch_pdl(k_quant_rows, dim3(row_tiles(a.n_rows), a.c.bh), dim3(kQrThreads), 0, s, a);
+    return launch_pdl(a.is_bf16 ? k_quant_rows<true> : k_quant_rows<false>, dim3(row_tiles(a.n_rows), a.c.bh), dim3(kQrThreads), 0, s, a);
 }
 
 }  // namespace pk
