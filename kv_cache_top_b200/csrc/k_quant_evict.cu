@@ -21,19 +21,21 @@ namespace pk {
 
 constexpr int kQeThreads = 512;
 constexpr int kQeWarps = kQeThreads / 32;
-constexpr int kQeBins = 2048;            // 11, 11 and 10 bits
+constexpr int kQeBins = 2048;            // digits of 11, 10 and 11 bits
 constexpr int kQeTile = 16384;           // slots in shared memory: two CTAs to an SM
 constexpr int kQeMaxCluster = 8;
 
 struct QeSmem {
     uint32_t key[kQeTile];
     uint16_t list[kQeTile];              // kept slots of the tile, from its first on
-    uint32_t hist[2][kQeBins];           // of the digit in turn: while the CTAs still read one, the next counts
+    uint32_t hist[kQeBins];              // of the digits 0 and 2,
+    uint32_t hist1[kQeBins / 2];         // and 1: while the CTAs still read one, the next counts
+    uint32_t keep[kQeThreads], tie[kQeThreads];   // bits of a group of 32 slots: those that stay, those that tie
     uint32_t ws[kQeWarps + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
-    uint32_t kept[kQeWarps], ties[kQeWarps];
 };
+static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of a tile");
 
 // ordered bits of a weight; NaN sorts below everything
 __device__ __forceinline__ uint32_t weight_key(float x)
@@ -125,31 +127,30 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     const int lo = all ? n : (int)a.sink, hi = all ? n : n - (int)a.recent;   // contested slots
     const uint32_t need = all ? 0u : (uint32_t)(a.budget - a.sink - a.recent);
     // this CTA's slots [c0, c1)
-    const int64_t run = ((n + ranks - 1) / ranks + 3) / 4 * 4;
-    const int64_t c0 = min((int64_t)n, rank * run), c1 = min((int64_t)n, c0 + run);
-    int64_t held = -1;                               // first slot of the tile in shared memory
-    auto tile = [&](int64_t c) {
+    const int run = (int)((((int64_t)n + ranks - 1) / ranks + 3) / 4 * 4);
+    const int c0 = (int)min((int64_t)n, (int64_t)rank * run), c1 = min(n, c0 + run);
+    int held = -1;                                   // first slot of the tile in shared memory
+    auto tile = [&](int c) {
         if (held == c || !need) return;
         __syncthreads();
-        load_tile(sm.key, acc, c, (int)min((int64_t)kQeTile, c1 - c), vec);
+        load_tile(sm.key, acc, c, min(kQeTile, c1 - c), vec);
         held = c;
         __syncthreads();
     };
-
     // threshold key: the need-th largest of the contested; left: how many of those equal to it stay
     uint32_t prefix = 0, left = need;
     if (need) {
 #pragma unroll 1
         for (int d = 0; d < 3; d++) {
-            const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
-            const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffffc00u;
-            uint32_t *hist = sm.hist[d & 1];
+            const int shift = d == 0 ? 21 : d == 1 ? 11 : 0, bins = d == 1 ? kQeBins / 2 : kQeBins;
+            const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffff800u;
+            uint32_t *hist = d == 1 ? sm.hist1 : sm.hist;
             for (int i = tid; i < bins; i += kQeThreads) hist[i] = 0;
             __syncthreads();
-            for (int64_t c = c0; c < c1; c += kQeTile) {
+            for (int c = c0; c < c1; c += kQeTile) {
                 tile(c);
-                const int first = (int)max((int64_t)0, lo - c), end = (int)min(min((int64_t)kQeTile, c1 - c), hi - c);
-#pragma unroll 4
+                const int first = max(0, lo - c), end = min(min(kQeTile, c1 - c), hi - c);
+#pragma unroll 8
                 for (int i = first + tid; i < end; i += kQeThreads) {
                     const uint32_t k = sm.key[i];
                     if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
@@ -159,7 +160,9 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
             // all CTAs' counts; thread t has bins [per t, per (t + 1))
             const int per = bins / kQeThreads;
             uint32_t mine[4] = {0, 0, 0, 0}, total = 0;
-            for (int w = 0; w < ranks; w++) {
+#pragma unroll
+            for (int w = 0; w < kQeMaxCluster; w++) {
+                if (w >= ranks) continue;
                 const uint32_t *h = cluster.map_shared_rank(hist, w) + per * tid;
                 if (per == 4) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(h);
@@ -187,44 +190,42 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
             __syncthreads();
         }
     }
-    // a warp's share of a tile: whole groups of 32 slots; what its lane's slot is: 2 kept, 1 tied, 0 dropped
-    auto kind = [&](int64_t c, int i) {
-        const int64_t s = c + i;
-        if (s >= c1) return 0;
-        if (s < lo || s >= hi) return 2;
-        if (!need) return 0;
-        const uint32_t k = sm.key[i];
-        return k > prefix ? 2 : k == prefix ? 1 : 0;
-    };
-    constexpr int kShare = kQeTile / kQeWarps;
-    auto count = [&](int64_t c, uint32_t *kept, uint32_t *ties) {
-        // shares of ceil(slots / warps) rounded up to groups
-        const int m = (int)min((int64_t)kQeTile, c1 - c), share = ((m + kQeWarps - 1) / kQeWarps + 31) / 32 * 32;
-        uint32_t x = 0, y = 0;
-        for (int i = warp * share; i < min(m, (warp + 1) * share); i += 32) {
-            const int k = kind(c, i + lane);
-            x += __popc(__ballot_sync(kFull, k == 2));
-            y += __popc(__ballot_sync(kFull, k == 1));
+    // keep and tie bits of a tile, by groups of 32 slots
+    auto mark = [&](int c) {
+        tile(c);
+        const int m = min(kQeTile, c1 - c), first = lo - c, end = hi - c;
+#pragma unroll 4
+        for (int i0 = 32 * warp; i0 < m; i0 += kQeThreads) {
+            const int i = i0 + lane;
+            const bool there = i < m, in = i >= first && i < end;
+            const uint32_t k = in && need ? sm.key[i] : 0u;
+            const uint32_t keep = __ballot_sync(kFull, there && (!in || (need && k > prefix)));
+            const uint32_t tie = __ballot_sync(kFull, there && in && need && k == prefix);
+            if (lane == 0) {
+                sm.keep[i0 >> 5] = keep;
+                sm.tie[i0 >> 5] = tie;
+            }
         }
-        *kept = x;
-        *ties = y;
-        return share;
+        __syncthreads();
     };
-    static_assert(kShare % 32 == 0, "shares are whole groups");
+    const bool one = c1 - c0 <= kQeTile;             // one tile: marked once
 
     // kept and tied slots of this CTA, and of those before it
     uint32_t before = 0, ties_before = 0;
     {
         uint32_t kept = 0, ties = 0;
-        for (int64_t c = c0; c < c1; c += kQeTile) {
-            uint32_t x, y;
-            tile(c);
-            count(c, &x, &y);
-            kept += x;
-            ties += y;
+        for (int c = c0; c < c1; c += kQeTile) {
+            mark(c);
+            if (32 * tid < c1 - c) {
+                kept += __popc(sm.keep[tid]);
+                ties += __popc(sm.tie[tid]);
+            }
+            if (!one) __syncthreads();
         }
         if (tid < 2) sm.count[tid] = 0;
         __syncthreads();
+        kept = __reduce_add_sync(kFull, kept);
+        ties = __reduce_add_sync(kFull, ties);
         if (lane == 0) {
             atomicAdd(&sm.count[0], kept);
             atomicAdd(&sm.count[1], ties);
@@ -237,42 +238,31 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         }
         before += min(ties_before, left);            // ties that stay are the lowest
     }
-    for (int64_t c = c0; c < c1; c += kQeTile) {
-        uint32_t x, y;
-        tile(c);
-        const int share = count(c, &x, &y), m = (int)min((int64_t)kQeTile, c1 - c);
-        if (lane == 0) {
-            sm.kept[warp] = x;
-            sm.ties[warp] = y;
-        }
+    cluster.barrier_arrive();                        // the other CTAs' memory has been read
+    for (int c = c0; c < c1; c += kQeTile) {
+        if (!one) mark(c);
+        const bool there = 32 * tid < c1 - c;
+        uint32_t keep = there ? sm.keep[tid] : 0u, tie = there ? sm.tie[tid] : 0u, total;
+        uint32_t rest = ties_before + block_excl_scan<kQeThreads>(__popc(tie), sm.ws, &total);
+        ties_before += total;
+        for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
+        sm.tie[tid] = block_excl_scan<kQeThreads>(__popc(keep), sm.ws, &total);     // the group's first place
+        sm.keep[tid] = keep;
         __syncthreads();
-        uint32_t at = 0, ties = ties_before, total = 0, all_ties = ties_before;   // of the warps before; of all
-        for (int w = 0; w < kQeWarps; w++) {
-            const uint32_t stay = min(all_ties + sm.ties[w], left) - min(all_ties, left);
-            if (w < warp) at += sm.kept[w] + stay, ties += sm.ties[w];
-            total += sm.kept[w] + stay;
-            all_ties += sm.ties[w];
-        }
-        for (int i = warp * share; i < min(m, (warp + 1) * share); i += 32) {
-            const int k = kind(c, i + lane);
-            const uint32_t tied = __ballot_sync(kFull, k == 1), below = (1u << lane) - 1;
-            const bool keep = k == 2 || (k == 1 && ties + __popc(tied & below) < left);
-            const uint32_t kept = __ballot_sync(kFull, keep);
-            if (keep) sm.list[at + __popc(kept & below)] = (uint16_t)(i + lane);
-            at += __popc(kept);
-            ties += __popc(tied);
+        for (int g = warp; 32 * g < c1 - c && g < kQeThreads; g += kQeWarps) {
+            const uint32_t w = sm.keep[g];
+            if (w >> lane & 1) sm.list[sm.tie[g] + __popc(w & ((1u << lane) - 1))] = (uint16_t)(32 * g + lane);
         }
         __syncthreads();
         move_rows(a, p, c, sm.list, (int)total, before);
         before += total;
-        ties_before = all_ties;
         __syncthreads();
     }
     const int64_t kept = all ? n : a.budget;
     if (a.keep)
         for (int64_t o = kept + rank * kQeThreads + tid; o < a.budget; o += (int64_t)ranks * kQeThreads) a.keep[p * a.budget + o] = -1;
     if (rank == 0 && tid == 0) a.dst.lens[p] = (int32_t)kept;
-    cluster.sync();                                  // the CTAs' counts have been read
+    cluster.barrier_wait();                          // and this CTA's by the others
 }
 
 cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)

@@ -31,7 +31,16 @@ __device__ __forceinline__ uint32_t quant_code(float x, float s, float inv)
 __device__ __forceinline__ uint32_t quant_scale_bits(float m)
 {
     if (!(m < INFINITY)) return 0x7fffu;
-    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(m, 7.0f)));
+    float q;
+    if (m > 1e-30f) {
+        // m / 7 to nearest by one step from the rounded reciprocal (Markstein 1990), exact for every normal m / 7
+        constexpr float kSeventh = 1.0f / 7.0f;
+        q = m * kSeventh;
+        q = fmaf(fmaf(-7.0f, q, m), kSeventh, q);
+    } else {
+        q = __fdiv_rn(m, 7.0f);
+    }
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(q));
 }
 
 // 8 consecutive elements i .. i + 7 of a bf16 or fp32 array, as they lie
@@ -96,27 +105,35 @@ __device__ __forceinline__ uint32_t quant_word(const Raw8 &raw, uint32_t *scale_
     *scale_bits = sb;
     const float s = bf16_bits_f32(sb);
     if (!(s > 0.0f)) return 0x88888888u;
+    uint32_t word = 0;
     if (s >= 1e-18f) {
         // x inv + 1.5 2^23 + 8 rounds to the code in the low bits; codes are joined by adding those bits, shifted, and
         // taking the constant parts off.  |x| < 7.02 s, so no clamp; a value within rounding of a border is seen by
-        // its remainder and goes the exact way.
+        // its remainder, which is exact (see quant_code)
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
         constexpr float kMagic = 12582920.0f;
-        uint32_t word = 0, base = 0;
-        float far = 0.0f;
+        uint32_t base = 0;
+        float y[8], far = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const float y = fmaf(x[e], inv, kMagic);
-            far = fmaxf(far, fabsf(fmaf(-(y - kMagic), s, x[e])));
-            word += __float_as_uint(y) << (4 * e);
+            y[e] = fmaf(x[e], inv, kMagic);
+            far = fmaxf(far, fabsf(fmaf(-(y[e] - kMagic), s, x[e])));
+            word += __float_as_uint(y[e]) << (4 * e);
             base += 0x4b400000u << (4 * e);
         }
-        if (2.0f * far < s) return word - base;
+        word -= base;
+        if (2.0f * far >= s) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float r = fmaf(-(y[e] - kMagic), s, x[e]), d = 2.0f * fabsf(r);
+                if (d > s || (d == s && (__float_as_uint(y[e]) & 1u))) word += (r > 0.0f ? 1u : 0xffffffffu) << (4 * e);
+            }
+        }
+        return word;
     }
-    const float up = s < 1e-18f ? 18446744073709551616.0f : 1.0f;     // 2^64: 1 / s stays finite
+    const float up = 18446744073709551616.0f;     // 2^64: 1 / s stays finite
     const float inv = __fdiv_rn(1.0f, s * up);
-    uint32_t word = 0;
 #pragma unroll
     for (int e = 0; e < 8; e++) word |= quant_code(x[e] * up, s * up, inv) << (4 * e);
     return word;
