@@ -8,8 +8,9 @@
 // places, and each CTA lists its kept slots and moves their rows.
 //
 // A run of up to kQeTile slots is read from HBM once and stays in shared
-// memory; a longer one is read again for each digit.  The order of the rows is
-// kept, so the result does not depend on the split.
+// memory; a longer one is read again for each digit.  Instructions bound the
+// select, so every step takes 4 slots a lane.  The order of the rows is kept,
+// so the result does not depend on the split.
 #include <cooperative_groups.h>
 
 #include "pk_launch.cuh"
@@ -30,7 +31,7 @@ struct QeSmem {
     uint16_t list[kQeTile];              // kept slots of the tile, from its first on
     uint32_t hist[kQeBins];              // of the digits 0 and 2,
     uint32_t hist1[kQeBins / 2];         // and 1: while the CTAs still read one, the next counts
-    uint32_t keep[kQeThreads], tie[kQeThreads];   // bits of a group of 32 slots: those that stay, those that tie
+    uint8_t marks[kQeTile / 4];          // of 4 slots: bits 0..3 those that stay, 4..7 those that tie
     uint32_t ws[kQeWarps + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
@@ -41,20 +42,6 @@ static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of a tile");
 __device__ __forceinline__ uint32_t weight_key(float x)
 {
     return x != x ? 0u : ord_f32(x + 0.0f);
-}
-
-// keys of slots [i0, i0 + count) to shared memory
-__device__ __forceinline__ void load_tile(uint32_t *key, const float *acc, int64_t i0, int count, bool vec)
-{
-    acc += i0;
-    if (vec) {
-#pragma unroll 4
-        for (int i = 4 * threadIdx.x; i + 4 <= count; i += 4 * kQeThreads) {
-            const float4 v = *reinterpret_cast<const float4 *>(acc + i);
-            *reinterpret_cast<uint4 *>(key + i) = make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
-        }
-    }
-    for (int i = (vec ? count / 4 * 4 : 0) + threadIdx.x; i < count; i += kQeThreads) key[i] = weight_key(acc[i]);
 }
 
 // Rows i0 + list[j] of src to slots o0 + j of dst, j < count, by the CTA's
@@ -130,13 +117,24 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     const int run = (int)((((int64_t)n + ranks - 1) / ranks + 3) / 4 * 4);
     const int c0 = (int)min((int64_t)n, (int64_t)rank * run), c1 = min(n, c0 + run);
     int held = -1;                                   // first slot of the tile in shared memory
-    auto tile = [&](int c) {
-        if (held == c || !need) return;
-        __syncthreads();
-        load_tile(sm.key, acc, c, min(kQeTile, c1 - c), vec);
-        held = c;
-        __syncthreads();
+    // 4 keys at slot i of the tile at c, of m slots: from shared memory, or (LOAD) from acc and kept there
+    auto keys = [&](uint32_t k[4], int c, int i, int m, bool load) {
+        if (load) {
+            const float *x = acc + c + i;
+            if (vec && i + 4 <= m) {
+                const float4 v = *reinterpret_cast<const float4 *>(x);
+                k[0] = weight_key(v.x), k[1] = weight_key(v.y), k[2] = weight_key(v.z), k[3] = weight_key(v.w);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) k[e] = i + e < m ? weight_key(x[e]) : 0u;
+            }
+            *reinterpret_cast<uint4 *>(sm.key + i) = make_uint4(k[0], k[1], k[2], k[3]);
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm.key + i);
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        }
     };
+
     // threshold key: the need-th largest of the contested; left: how many of those equal to it stay
     uint32_t prefix = 0, left = need;
     if (need) {
@@ -148,13 +146,20 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
             for (int i = tid; i < bins; i += kQeThreads) hist[i] = 0;
             __syncthreads();
             for (int c = c0; c < c1; c += kQeTile) {
-                tile(c);
-                const int first = max(0, lo - c), end = min(min(kQeTile, c1 - c), hi - c);
-#pragma unroll 8
-                for (int i = first + tid; i < end; i += kQeThreads) {
-                    const uint32_t k = sm.key[i];
-                    if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+                const int m = min(kQeTile, c1 - c), first = lo - c, end = min(m, hi - c);
+                const bool load = held != c;
+                if (load && held >= 0) __syncthreads();          // the tile before is no longer read
+#pragma unroll 4
+                for (int i = 4 * tid; i < m; i += 4 * kQeThreads) {
+                    uint32_t k[4];
+                    keys(k, c, i, m, load);
+                    const bool in = i >= first && i + 4 <= end;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if ((in || (i + e >= first && i + e < end)) && (k[e] & above) == prefix)
+                            atomicAdd(&hist[(k[e] >> shift) & (bins - 1)], 1u);
                 }
+                held = c;
             }
             cluster.sync();
             // all CTAs' counts; thread t has bins [per t, per (t + 1))
@@ -190,23 +195,48 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
             __syncthreads();
         }
     }
-    // keep and tie bits of a tile, by groups of 32 slots
+    // marks of a tile
     auto mark = [&](int c) {
-        tile(c);
         const int m = min(kQeTile, c1 - c), first = lo - c, end = hi - c;
+        const bool load = held != c;
+        __syncthreads();                             // the marks, and the tile before, are no longer read
 #pragma unroll 4
-        for (int i0 = 32 * warp; i0 < m; i0 += kQeThreads) {
-            const int i = i0 + lane;
-            const bool there = i < m, in = i >= first && i < end;
-            const uint32_t k = in && need ? sm.key[i] : 0u;
-            const uint32_t keep = __ballot_sync(kFull, there && (!in || (need && k > prefix)));
-            const uint32_t tie = __ballot_sync(kFull, there && in && need && k == prefix);
-            if (lane == 0) {
-                sm.keep[i0 >> 5] = keep;
-                sm.tie[i0 >> 5] = tie;
+        for (int i = 4 * tid; i < m; i += 4 * kQeThreads) {
+            uint32_t keep = 0, tie = 0;
+            if (i < end && i + 4 > first && need) {
+                uint32_t k[4];
+                keys(k, c, i, m, load);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    keep |= (uint32_t)(k[e] > prefix) << e;
+                    tie |= (uint32_t)(k[e] == prefix) << e;
+                }
             }
+            if (i < first || i + 4 > end || i + 4 > m) {         // slots that stay whatever their weight, or are none
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int j = i + e;
+                    if (j < m && j >= first && j < end) continue;
+                    keep = (keep & ~(1u << e)) | (uint32_t)(j < m) << e;
+                    tie &= ~(1u << e);
+                }
+            }
+            sm.marks[i >> 2] = (uint8_t)(keep | tie << 4);
         }
+        if (need) held = c;
         __syncthreads();
+    };
+    // keep and tie bits of the thread's 32 slots of a tile
+    auto marked = [&](int c, uint32_t *keep, uint32_t *tie) {
+        uint2 w = make_uint2(0, 0);
+        const int m = min(kQeTile, c1 - c);
+        if (32 * tid < m) w = *reinterpret_cast<const uint2 *>(sm.marks + 8 * tid);
+        auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
+        *keep = nibbles(w.x) | nibbles(w.y) << 16;
+        *tie = nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16;
+        const uint32_t there = 32 * tid + 32 <= m ? 0xffffffffu : 32 * tid < m ? (1u << (m & 31)) - 1 : 0u;   // marks behind the last slot are old
+        *keep &= there;
+        *tie &= there;
     };
     const bool one = c1 - c0 <= kQeTile;             // one tile: marked once
 
@@ -215,12 +245,11 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     {
         uint32_t kept = 0, ties = 0;
         for (int c = c0; c < c1; c += kQeTile) {
+            uint32_t keep, tie;
             mark(c);
-            if (32 * tid < c1 - c) {
-                kept += __popc(sm.keep[tid]);
-                ties += __popc(sm.tie[tid]);
-            }
-            if (!one) __syncthreads();
+            marked(c, &keep, &tie);
+            kept += __popc(keep);
+            ties += __popc(tie);
         }
         if (tid < 2) sm.count[tid] = 0;
         __syncthreads();
@@ -241,18 +270,13 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     cluster.barrier_arrive();                        // the other CTAs' memory has been read
     for (int c = c0; c < c1; c += kQeTile) {
         if (!one) mark(c);
-        const bool there = 32 * tid < c1 - c;
-        uint32_t keep = there ? sm.keep[tid] : 0u, tie = there ? sm.tie[tid] : 0u, total;
+        uint32_t keep, tie, total;
+        marked(c, &keep, &tie);
         uint32_t rest = ties_before + block_excl_scan<kQeThreads>(__popc(tie), sm.ws, &total);
         ties_before += total;
         for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
-        sm.tie[tid] = block_excl_scan<kQeThreads>(__popc(keep), sm.ws, &total);     // the group's first place
-        sm.keep[tid] = keep;
-        __syncthreads();
-        for (int g = warp; 32 * g < c1 - c && g < kQeThreads; g += kQeWarps) {
-            const uint32_t w = sm.keep[g];
-            if (w >> lane & 1) sm.list[sm.tie[g] + __popc(w & ((1u << lane) - 1))] = (uint16_t)(32 * g + lane);
-        }
+        uint32_t at = block_excl_scan<kQeThreads>(__popc(keep), sm.ws, &total);
+        for (; keep; keep &= keep - 1) sm.list[at++] = (uint16_t)(32 * tid + __ffs(keep) - 1);
         __syncthreads();
         move_rows(a, p, c, sm.list, (int)total, before);
         before += total;
