@@ -29,14 +29,15 @@ constexpr int kQeMaxCluster = 8;
 struct QeSmem {
     uint32_t key[kQeTile];
     uint16_t list[kQeTile];              // kept slots of the tile, from its first on
-    uint32_t hist[kQeBins];              // of the digits 0 and 2,
-    uint32_t hist1[kQeBins / 2];         // and 1: while the CTAs still read one, the next counts
-    uint8_t marks[kQeTile / 4];          // of 4 slots: bits 0..3 those that stay, 4..7 those that tie
+    uint32_t hist[kQeBins];              // this CTA's counts
+    uint32_t sums[kQeBins];              // all CTAs' counts; afterwards the marks of 4 slots each: bits 0..3 those that
+                                         // stay, 4..7 those that tie
     uint32_t ws[kQeWarps + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
 };
 static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of a tile");
+static_assert(kQeTile / 4 <= kQeBins * 4, "the marks fit the sums");
 
 // ordered bits of a weight; NaN sorts below everything
 __device__ __forceinline__ uint32_t weight_key(float x)
@@ -142,8 +143,7 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         for (int d = 0; d < 3; d++) {
             const int shift = d == 0 ? 21 : d == 1 ? 11 : 0, bins = d == 1 ? kQeBins / 2 : kQeBins;
             const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffff800u;
-            uint32_t *hist = d == 1 ? sm.hist1 : sm.hist;
-            for (int i = tid; i < bins; i += kQeThreads) hist[i] = 0;
+            for (int i = tid; i < bins; i += kQeThreads) sm.hist[i] = 0;
             __syncthreads();
             for (int c = c0; c < c1; c += kQeTile) {
                 const int m = min(kQeTile, c1 - c), first = lo - c, end = min(m, hi - c);
@@ -153,30 +153,42 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
                 for (int i = 4 * tid; i < m; i += 4 * kQeThreads) {
                     uint32_t k[4];
                     keys(k, c, i, m, load);
-                    const bool in = i >= first && i + 4 <= end;
+                    auto count = [&](int e) { atomicAdd(&sm.hist[(k[e] >> shift) & (bins - 1)], 1u); };
+                    if (i >= first && i + 4 <= end) {
+                        if (d == 0) {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) count(e);
+                            continue;
+                        }
+                        bool any = false;            // few agree with the digits before
+#pragma unroll
+                        for (int e = 0; e < 4; e++) any |= (k[e] & above) == prefix;
+                        if (!any) continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        if ((in || (i + e >= first && i + e < end)) && (k[e] & above) == prefix)
-                            atomicAdd(&hist[(k[e] >> shift) & (bins - 1)], 1u);
+                        if (i + e >= first && i + e < end && (k[e] & above) == prefix) count(e);
                 }
                 held = c;
             }
             cluster.sync();
-            // all CTAs' counts; thread t has bins [per t, per (t + 1))
+            // each CTA joins the counts of its share of the bins and gives all the sums
+            const int share = bins / ranks;
+            for (int i = tid; i < share; i += kQeThreads) {
+                uint32_t x[kQeMaxCluster], v = 0;
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist, w)[rank * share + i] : 0u;
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++) v += x[w];
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++)
+                    if (w < ranks) cluster.map_shared_rank(sm.sums, w)[rank * share + i] = v;
+            }
+            cluster.sync();
+            // thread t has bins [per t, per (t + 1))
             const int per = bins / kQeThreads;
             uint32_t mine[4] = {0, 0, 0, 0}, total = 0;
-#pragma unroll
-            for (int w = 0; w < kQeMaxCluster; w++) {
-                if (w >= ranks) continue;
-                const uint32_t *h = cluster.map_shared_rank(hist, w) + per * tid;
-                if (per == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(h);
-                    mine[0] += v.x, mine[1] += v.y, mine[2] += v.z, mine[3] += v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(h);
-                    mine[0] += v.x, mine[1] += v.y;
-                }
-            }
+            for (int e = 0; e < per; e++) mine[e] = sm.sums[per * tid + e];
             total = mine[0] + mine[1] + mine[2] + mine[3];
             uint32_t sum;
             uint32_t over = block_excl_scan<kQeThreads>(total, sm.ws, &sum);
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
                     tie &= ~(1u << e);
                 }
             }
-            sm.marks[i >> 2] = (uint8_t)(keep | tie << 4);
+            reinterpret_cast<uint8_t *>(sm.sums)[i >> 2] = (uint8_t)(keep | tie << 4);
         }
         if (need) held = c;
         __syncthreads();
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
     auto marked = [&](int c, uint32_t *keep, uint32_t *tie) {
         uint2 w = make_uint2(0, 0);
         const int m = min(kQeTile, c1 - c);
-        if (32 * tid < m) w = *reinterpret_cast<const uint2 *>(sm.marks + 8 * tid);
+        if (32 * tid < m) w = reinterpret_cast<const uint2 *>(sm.sums)[tid];
         auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
         *keep = nibbles(w.x) | nibbles(w.y) << 16;
         *tie = nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16;
