@@ -511,25 +511,29 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
 }
 
 // Merge of a pair's partial results (CTAs x < G: head x) and its part of acc
-// (CTAs x >= G: keys [(x - G) kQmKeys, ...)).
+// (CTAs x >= G: keys [(x - G) kQmKeys, ...)).  The lengths are read before the
+// attention kernel has ended: it waited for whatever wrote them.
 __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
 {
     __shared__ uint32_t s_sum[kQmThreads / 32];
     __shared__ float s_lse[kMaxGroup];
     const int tid = threadIdx.x, p = blockIdx.y, G = a.G;
-    pdl_wait();
     const int n = quant_len(a.c, p);
     const bool is_out = (int)blockIdx.x < G;
     const int64_t k0 = (int64_t)((int)blockIdx.x - G) * kQmKeys;
     if (!is_out && k0 >= n) return;
+    uint32_t total = 0, first = 0;
+    if (n > 0) {
+        total = count_blocks<kQmThreads>(a.c, a.c.bh, s_sum);
+        first = count_blocks<kQmThreads>(a.c, p, s_sum);
+    }
+    pdl_wait();
     if (is_out && blockIdx.x == 0 && tid == 0 && quant_len_bad(a.c, p)) quant_devchk(a.c.status, p);
     if (n == 0) {
         if (tid < kD) a.out[((int64_t)p * G + blockIdx.x) * kD + tid] = 0.0f;
         if (tid == 0 && a.lse) a.lse[(int64_t)p * G + blockIdx.x] = -INFINITY;
         return;
     }
-    const uint32_t total = count_blocks<kQmThreads>(a.c, a.c.bh, s_sum);
-    const uint32_t first = count_blocks<kQmThreads>(a.c, p, s_sum);
     const uint32_t share = (uint32_t)quant_share(total, a.workers, kQaMinShare);
     const int w0 = (int)(first / share), w1 = (int)((first + block_count(a.c, p) - 1) / share);
     const float *part = a.part + (int64_t)(p + w0) * G * kQPart;
@@ -549,6 +553,7 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
         if (is_out) {
             if (tid < kD) {
                 float o = 0.0f;
+#pragma unroll 4
                 for (int s = 0; s < ns; s++)
                     o = fmaf(exp2f(pg[(int64_t)s * G * kQPart] - ref), pg[(int64_t)s * G * kQPart - kD + tid], o);
                 a.out[((int64_t)p * G + g) * kD + tid] = l == 0.0f ? 0.0f : o / l;
@@ -560,11 +565,37 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
     }
     if (is_out) return;
     __syncthreads();
-    for (int64_t k = k0 + tid; k < min((int64_t)n, k0 + kQmKeys); k += kQmThreads) {
+    // 4 keys a thread: all heads' logits and the sums in flight at once
+    float *acc = a.c.acc + (int64_t)p * a.c.n_cap;
+    const bool vec = (uintptr_t)acc % 16 == 0;
+#pragma unroll 2
+    for (int64_t k = k0 + 4 * tid; k < min((int64_t)n, k0 + kQmKeys); k += 4 * kQmThreads) {
         const float *z = a.logits + ((int64_t)p * (a.c.n_cap / kQKeys) + k / kQKeys) * G * kQKeys + k % kQKeys;
-        float sum = 0.0f;
-        for (int g = 0; g < G; g++) sum += exp2f(z[g * kQKeys] - s_lse[g]);
-        a.c.acc[(int64_t)p * a.c.n_cap + k] += sum;
+        float4 x[kMaxGroup];
+#pragma unroll
+        for (int g = 0; g < kMaxGroup; g++)
+            if (g < G) x[g] = __ldcs(reinterpret_cast<const float4 *>(z + g * kQKeys));
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const bool whole = vec && k + 4 <= n;
+        if (whole) sum = *reinterpret_cast<const float4 *>(acc + k);
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int g = 0; g < kMaxGroup; g++)
+            if (g < G) {
+                const float lse = s_lse[g];
+                w.x += ex2(x[g].x - lse);
+                w.y += ex2(x[g].y - lse);
+                w.z += ex2(x[g].z - lse);
+                w.w += ex2(x[g].w - lse);
+            }
+        if (whole) {
+            *reinterpret_cast<float4 *>(acc + k) = make_float4(sum.x + w.x, sum.y + w.y, sum.z + w.z, sum.w + w.w);
+        } else {
+            acc[k] += w.x;
+            if (k + 1 < n) acc[k + 1] += w.y;
+            if (k + 2 < n) acc[k + 2] += w.z;
+            if (k + 3 < n) acc[k + 3] += w.w;
+        }
     }
 }
 
