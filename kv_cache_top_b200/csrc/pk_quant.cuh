@@ -56,11 +56,10 @@ struct QuantRowsArgs {
     int32_t vec;             // rows are 16-byte aligned
 };
 
-// Attention splits the pairs' blocks, laid end to end, evenly over the CTAs
-// ("workers") whatever the lengths: worker w takes blocks [w share, (w+1)
-// share) of the total.  A pair's segment in a worker leaves one partial result
-// in slot pair + worker: consecutive segments differ in at least one of the
-// two, so slots are never shared.
+// Attention splits the pairs' blocks, laid end to end, over the CTAs
+// ("workers") whatever the lengths.  A pair's segment in a worker leaves one
+// partial result in slot pair + worker: consecutive segments differ in at
+// least one of the two, so slots are never shared.
 constexpr int kQMaxWorkers = 1024;
 constexpr int kQPart = kD + 2;           // floats of a head's partial: sums, then reference maximum and weight sum
 
@@ -73,6 +72,7 @@ struct QuantAttendArgs {
     float *logits;           // [bh][n_cap / 32][G][32] (log2 units) when accumulating, else null
     int32_t G, is_bf16, accumulate;
     int32_t workers;
+    int32_t outs;            // merge kernel: CTAs per pair that write outputs
     float scale2;            // softmax scale * log2(e)
 };
 
