@@ -568,3 +568,75 @@ def test_two_streams_with_their_own_workspaces(pk):
             K, V = ref.values(blocks[p])
             o, _, _, eo, _, _ = ref.attend(q[p].double().cpu().numpy(), K[:n], V[:n])
             assert np.all(np.abs(out[p].cpu().double().numpy() - o) <= eo)
+
+
+# ---------------------------------------------------------------- the bounded decode cache
+def test_bounded_cache_refuses_bad_sizes(pk):
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    K = torch.zeros(1, 2, 5, D)
+    for kw in (dict(budget=0), dict(budget=4, sink=3, recent=2), dict(budget=4, sink=-1, recent=0), dict(budget=4, sink=0, recent=0, update=0),
+               dict(budget=4, sink=0, recent=0, group=9)):
+        with pytest.raises(ValueError):
+            BoundedCache(K, K, **{**dict(group=2), **kw})
+    with pytest.raises(ValueError):
+        BoundedCache(K.half(), K.half(), group=2, budget=4, sink=0, recent=0)
+    with pytest.raises(ValueError):
+        BoundedCache(K[0], K[0], group=2, budget=4, sink=0, recent=0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,T0,budget,sink,recent,update", [
+    ("bf16", 40, 24, 2, 8, 16), ("f32", 300, 64, 4, 20, 33), ("bf16", 0, 8, 0, 0, 5), ("bf16", 33, 32, 32, 0, 1),
+])
+def test_bounded_cache_steps(pk, dtype, T0, budget, sink, recent, update):
+    """A run of steps against a plain one: the stored values, the attention of every step, the accumulated weights and
+    the tokens that each eviction keeps."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    td, _ = dt(pk, dtype)
+    rng = np.random.default_rng(T0 + budget)
+    B, H, G = 2, 2, 3
+    bh = B * H
+    rows = [make_rows(rng, bh * T0, td).view(B, H, T0, D) for _ in range(2)]
+    c = BoundedCache(rows[0].cuda(), rows[1].cuda(), group=G, budget=budget, sink=sink, recent=recent, update=update)
+    held = [[ref.stored(x.view(bh, T0, D)[p].float().numpy())[2] for x in rows] for p in range(bh)]
+    pos = [np.arange(T0) for _ in range(bh)]
+    acc = [np.zeros(T0) for _ in range(bh)]
+    evictions = 0
+
+    def check(q, out):
+        out, lse = out.view(bh, G, D).cpu().double().numpy(), c.lse.view(bh, G).cpu().double().numpy()
+        got = c.weights.reshape(bh, -1).cpu().double().numpy()
+        for p in range(bh):
+            o, l, w, eo, el, ew = ref.attend(q.view(bh, G, D)[p].double().numpy(), held[p][0], held[p][1])
+            assert np.all(np.abs(out[p] - o) <= eo) and (not len(w[0]) or np.all(np.abs(lse[p] - l) <= el))
+            acc[p] = acc[p] + w.sum(0)
+            # every step's weights carry their bound and the sum a rounding: a relative part of what has been added
+            tol = (ew.max(initial=0) * 2 + (G + 2) * ref.U * (c.T + 5)) * acc[p] + 1e-37
+            assert np.all(np.abs(got[p] - acc[p]) <= tol)
+            acc[p] = got[p].copy()                    # the next eviction goes by the kernel's sums
+
+    for _ in range(3):
+        q = make_rows(rng, bh * G, td).view(B, H * G, D)
+        check(q, c.observe(q.cuda()))
+    for t in range(3 * update + budget + 5):
+        if c.n >= budget + update:
+            evictions += 1
+            for p in range(bh):
+                keep = ref.evict(acc[p], c.n, budget, sink, recent)
+                held[p] = [x[keep] for x in held[p]]
+                pos[p], acc[p] = pos[p][keep], acc[p][keep]
+        new = [make_rows(rng, bh, td).view(B, H, 1, D) for _ in range(2)]
+        q = make_rows(rng, bh * G, td).view(B, H * G, D)
+        out = c.step(q.cuda(), new[0].cuda(), new[1].cuda())
+        for p in range(bh):
+            held[p] = [np.concatenate([a, ref.stored(x.view(bh, 1, D)[p].float().numpy())[2]]) for a, x in zip(held[p], new)]
+            pos[p], acc[p] = np.append(pos[p], T0 + t), np.append(acc[p], 0.0)
+        check(q, out)
+        assert c.evictions == evictions and c.T == T0 + t + 1
+    assert evictions >= 3
+    k, v = c.rows()
+    where = c.positions.reshape(bh, -1).cpu().numpy()
+    for p in range(bh):
+        assert np.array_equal(where[p], pos[p])
+        for got, want in ((k, held[p][0]), (v, held[p][1])):
+            assert torch.equal(got.view(bh, -1, D)[p].cpu(), torch.from_numpy(want.astype(np.float32)).to(td))
