@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     QaSmem &sm = *reinterpret_cast<QaSmem *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, G = a.G;
     if (lane < kQaStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sm.bar[warp][lane])) : "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     pdl_wait();
+    asm volatile("fence.proxy.async;" ::: "memory");     // the barriers, and rows that earlier kernels wrote
     pdl_trigger();
 
     // this worker's blocks [x0, end) of all, and the pair of the first
