@@ -2,18 +2,22 @@
 //
 // Of a pair's keys the first `sink` and the last `recent` stay; of the others
 // the heaviest, ties to the lower slots.  A radix select over the ordered bits
-// of acc (three digits) gives the threshold weight; the kept slots are listed
-// and their rows moved.
+// of acc (digits of 11, 10 and 11 bits) gives the threshold weight; the kept
+// slots are listed in order and their rows moved.  Instructions bound the
+// select, so every step takes 4 slots a lane.  The result does not depend on
+// how slots are split.
 //
-// A pair whose slots fit a CTA's shared memory is selected by each of its CTAs
-// for itself, and each moves a share of the rows: reading acc again costs less
-// than cluster barriers (64 pairs of 1600 keys: 19 us of 30 were those).  A
-// longer one is a cluster's: each CTA has a run of slots, their histograms are
-// joined through distributed shared memory, and their counts of kept keys and
-// ties give each its places.  A run of up to kQeTile slots is read from HBM
-// once; a longer one is read again for each digit.  Instructions bound the
-// select, so every step takes 4 slots a lane.  The order of the rows is kept,
-// so the result does not depend on the split.
+// k_quant_evict, up to kQeTile slots a pair: they stay in a CTA's shared
+// memory.  Each of a pair's CTAs selects for itself and moves a share of the
+// rows: reading acc again costs less than cluster barriers (64 pairs of 1600
+// keys: 24 us for 29).
+// k_quant_select, k_quant_gather, longer pairs: a cluster selects, each CTA a
+// run of slots that it reads for every digit (from L2 after the first time);
+// histograms are joined through distributed shared memory, and a CTA's own
+// counts above the threshold give its places.  The list of kept slots goes to
+// `keep`, or to dst's acc (whose weights the gather writes in their place), and
+// a second kernel moves the rows, all SMs' memory pipes full.  With neither,
+// the cluster moves them itself.
 #include <cooperative_groups.h>
 
 #include "pk_launch.cuh"
@@ -24,24 +28,42 @@ namespace cg = cooperative_groups;
 namespace pk {
 
 constexpr int kQeThreads = 512;
-constexpr int kQeWarps = kQeThreads / 32;
-constexpr int kQeBins = 2048;            // digits of 11, 10 and 11 bits
+constexpr int kQeBins = 2048;
 constexpr int kQeTile = 16384;           // slots in shared memory: two CTAs to an SM
+constexpr int kQsThreads = 256;          // select
+constexpr int kQsPer = 16;               // consecutive slots a thread lists at once
+constexpr int kQsChunk = kQsPer * kQsThreads;
 constexpr int kQeMaxCluster = 8;
 
 struct QeSmem {
     uint32_t key[kQeTile];               // weights as they come, then their keys
-    uint16_t list[kQeTile];              // kept slots of the tile, from its first on
+    uint16_t list[kQeTile];              // kept slots
+    uint32_t hist[kQeBins];
+    uint8_t marks[kQeTile / 4];          // of 4 slots: bits 0..3 those that stay, 4..7 those that tie
+    uint32_t ws[kQeThreads / 32 + 1];
+    uint32_t digit, left;
+    unsigned long long bar;              // bulk copies of the weights
+};
+static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots");
+
+struct QsSmem {
     uint32_t hist[kQeBins];              // this CTA's counts
-    uint32_t sums[kQeBins];              // all CTAs' counts; afterwards the marks of 4 slots each: bits 0..3 those that
-                                         // stay, 4..7 those that tie
-    uint32_t ws[kQeWarps + 1];
+    uint32_t sums[kQeBins];              // all CTAs' counts
+    uint32_t ws[kQsThreads / 32 + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
-    unsigned long long bar;              // bulk copies of a tile
+    int list[kQsChunk];                  // kept slots of a chunk, when this kernel moves the rows
 };
-static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of a tile");
-static_assert(kQeTile / 4 <= kQeBins * 4, "the marks fit the sums");
+
+// digit d of the select: its place, its bins, and the bits above it
+struct Digit {
+    int shift, bins;
+    uint32_t above;
+};
+__device__ __forceinline__ Digit digit_of(int d)
+{
+    return d == 0 ? Digit{21, 2048, 0u} : d == 1 ? Digit{11, 1024, 0xffe00000u} : Digit{0, 2048, 0xfffff800u};
+}
 
 // ordered bits of a weight; NaN sorts below everything
 __device__ __forceinline__ uint32_t weight_key(float x)
@@ -49,269 +71,297 @@ __device__ __forceinline__ uint32_t weight_key(float x)
     return x != x ? 0u : ord_f32(x + 0.0f);
 }
 
-// Rows i0 + list[j] of src to slots o0 + j of dst, j < count, by the CTA's
-// warps: 32 rows at a time, 16 bytes a lane.
-__device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, int64_t i0, const uint16_t *list, int count, int64_t o0)
+// The bin of the left-th largest key by the counts `sums`: *digit, and in *left
+// its rank within the bin; over a CTA of NT threads.
+template <int NT>
+__device__ __forceinline__ void find_digit(const uint32_t *sums, int bins, uint32_t *ws, uint32_t left, uint32_t *digit, uint32_t *rank)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kMost = kQeBins / NT;
+    const int per = bins / NT, tid = threadIdx.x;
+    uint32_t mine[kMost], total = 0, sum;
+#pragma unroll
+    for (int e = 0; e < kMost; e++) {
+        mine[e] = e < per ? sums[per * tid + e] : 0u;
+        total += mine[e];
+    }
+    uint32_t over = block_excl_scan<NT>(total, ws, &sum);
+    over = sum - over - total;           // keys in the bins above the thread's
+#pragma unroll
+    for (int e = kMost - 1; e >= 0; e--) {
+        if (over < left && over + mine[e] >= left) {
+            *digit = per * tid + e;
+            *rank = left - over;
+        }
+        over += mine[e];
+    }
+    __syncthreads();
+}
+
+// Up to 32 rows to slots o .. o + m - 1 of dst by a warp, lane j < m with the
+// source slot of row j: 16 bytes a lane, all loads in flight.
+__device__ __forceinline__ void move_rows(const QuantEvictArgs &a, int p, int slot, int m, int64_t o0, bool write_keep)
+{
+    const int lane = threadIdx.x & 31;
     const uint8_t *src = a.src.blocks + (int64_t)p * (a.src.n_cap / kQKeys) * kQBlock;
     uint8_t *dst = a.dst.blocks + (int64_t)p * (a.dst.n_cap / kQKeys) * kQBlock;
-    const float *acc = a.src.acc + (int64_t)p * a.src.n_cap;
-    for (int j0 = 32 * warp; j0 < count; j0 += kQeThreads) {
-        const int m = min(32, count - j0);
-        uint4 kc[4], vc[4];
-        uint2 ks = make_uint2(0, 0), vs = ks;
-        float w = 0.0f;
-        int slot = 0;
+    uint4 kc[4], vc[4];
+    uint2 ks = make_uint2(0, 0), vs = ks;
+    float w = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {        // rows 8i + lane / 4, quarter lane % 4
-            const int j = 8 * i + (lane >> 2);
-            if (j < m) {
-                const int x = (int)i0 + list[j0 + j];
-                const uint8_t *b = src + (int64_t)(x / kQKeys) * kQBlock + x % kQKeys * kQRow;
-                kc[i] = __ldcs(reinterpret_cast<const uint4 *>(b) + (lane & 3));
-                // chunk places of V differ by the turn of the slot: taken in the order of slots with no turn
-                vc[i] = __ldcs(reinterpret_cast<const uint4 *>(b + kQOffV) + ((lane & 3) ^ (v_turn(x) >> 1)));
-            }
+    for (int i = 0; i < 4; i++) {        // rows 8i + lane / 4, quarter lane % 4
+        const int j = 8 * i + (lane >> 2), x = __shfl_sync(kFull, slot, j);
+        if (j < m) {
+            const uint8_t *b = src + (int64_t)(x / kQKeys) * kQBlock + x % kQKeys * kQRow;
+            kc[i] = __ldcs(reinterpret_cast<const uint4 *>(b) + (lane & 3));
+            // chunk places of V differ by the turn of the slot: taken in the order of slots with no turn
+            vc[i] = __ldcs(reinterpret_cast<const uint4 *>(b + kQOffV) + ((lane & 3) ^ (v_turn(x) >> 1)));
         }
-        if (lane < m) {
-            slot = (int)i0 + list[j0 + lane];
-            const uint8_t *b = src + (int64_t)(slot / kQKeys) * kQBlock;
-            ks = *reinterpret_cast<const uint2 *>(b + kQOffKs + 8 * (slot % kQKeys));
-            vs = *reinterpret_cast<const uint2 *>(b + kQOffVs + 8 * (slot % kQKeys));
-            if (a.dst.acc) w = acc[slot];
-        }
+    }
+    if (lane < m) {
+        const uint8_t *b = src + (int64_t)(slot / kQKeys) * kQBlock;
+        ks = *reinterpret_cast<const uint2 *>(b + kQOffKs + 8 * (slot % kQKeys));
+        vs = *reinterpret_cast<const uint2 *>(b + kQOffVs + 8 * (slot % kQKeys));
+        if (a.dst.acc) w = a.src.acc[(int64_t)p * a.src.n_cap + slot];
+    }
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int j = 8 * i + (lane >> 2);
-            if (j < m) {
-                const int64_t o = o0 + j0 + j;
-                const int y = (int)(o % kQKeys);
-                uint8_t *b = dst + o / kQKeys * kQBlock + y * kQRow;
-                reinterpret_cast<uint4 *>(b)[lane & 3] = kc[i];
-                reinterpret_cast<uint4 *>(b + kQOffV)[(lane & 3) ^ (v_turn(y) >> 1)] = vc[i];
-            }
+    for (int i = 0; i < 4; i++) {
+        const int j = 8 * i + (lane >> 2);
+        if (j < m) {
+            const int64_t o = o0 + j;
+            const int y = (int)(o % kQKeys);
+            uint8_t *b = dst + o / kQKeys * kQBlock + y * kQRow;
+            reinterpret_cast<uint4 *>(b)[lane & 3] = kc[i];
+            reinterpret_cast<uint4 *>(b + kQOffV)[(lane & 3) ^ (v_turn(y) >> 1)] = vc[i];
         }
-        if (lane < m) {
-            const int64_t o = o0 + j0 + lane;
-            uint8_t *b = dst + o / kQKeys * kQBlock;
-            *reinterpret_cast<uint2 *>(b + kQOffKs + 8 * (o % kQKeys)) = ks;
-            *reinterpret_cast<uint2 *>(b + kQOffVs + 8 * (o % kQKeys)) = vs;
-            if (a.dst.acc) a.dst.acc[p * a.dst.n_cap + o] = w;
-            if (a.keep) a.keep[p * a.budget + o] = slot;
-        }
+    }
+    if (lane < m) {
+        const int64_t o = o0 + lane;
+        uint8_t *b = dst + o / kQKeys * kQBlock;
+        *reinterpret_cast<uint2 *>(b + kQOffKs + 8 * (o % kQKeys)) = ks;
+        *reinterpret_cast<uint2 *>(b + kQOffVs + 8 * (o % kQKeys)) = vs;
+        if (a.dst.acc) a.dst.acc[p * a.dst.n_cap + o] = w;
+        if (write_keep && a.keep) a.keep[p * a.budget + o] = slot;
     }
 }
 
-template <bool ALONE>
+// Slots of a pair: all of them stay, or `need` of the contested [lo, hi) and the others.
+struct Contest {
+    int n, lo, hi;
+    uint32_t need;
+};
+__device__ __forceinline__ Contest contest(const QuantEvictArgs &a, int p)
+{
+    const int n = quant_len(a.src, p);
+    if (n <= a.budget) return Contest{n, n, n, 0u};
+    return Contest{n, (int)a.sink, n - (int)a.recent, (uint32_t)(a.budget - a.sink - a.recent)};
+}
+
+// What is the same in both ways: the length, the end of the list, the check.
+__device__ __forceinline__ void finish(const QuantEvictArgs &a, int p, int n, int threads)
+{
+    const int64_t kept = min((int64_t)n, a.budget);
+    if (a.keep)
+        for (int64_t o = kept + (int)blockIdx.x * threads + (int)threadIdx.x; o < a.budget; o += (int64_t)gridDim.x * threads)
+            a.keep[p * a.budget + o] = -1;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.dst.lens[p] = (int32_t)kept;
+        if (quant_len_bad(a.src, p)) quant_devchk(a.src.status, p);
+    }
+}
+
 __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     QeSmem &sm = *reinterpret_cast<QeSmem *>(smem_raw);
-    cg::cluster_group cluster = cg::this_cluster();
     const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = ALONE ? 0 : (int)cluster.block_rank(), ranks = ALONE ? 1 : (int)cluster.num_blocks();
-    auto sync = [&]() { if (ALONE) __syncthreads(); else cluster.sync(); };
-    if (tid == 0) {
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"((uint32_t)__cvta_generic_to_shared(&sm.bar)) : "memory");
-    }
-    uint32_t phase = 0;
-    bool late = false;
+    const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&sm.bar);
+    if (tid == 0) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
     pdl_wait();
-    const int n = quant_len(a.src, p);
-    if (blockIdx.x == 0 && tid == 0 && quant_len_bad(a.src, p)) quant_devchk(a.src.status, p);
+    const Contest q = contest(a, p);
+    const int n = q.n;
     const float *acc = a.src.acc + (int64_t)p * a.src.n_cap;
-    const bool vec = (uintptr_t)acc % 16 == 0;       // n_cap is a multiple of 32: the same for every pair
-    const bool all = n <= a.budget;
-    const int lo = all ? n : (int)a.sink, hi = all ? n : n - (int)a.recent;   // contested slots
-    const uint32_t need = all ? 0u : (uint32_t)(a.budget - a.sink - a.recent);
-    // this CTA's slots [c0, c1)
-    const int run = (int)((((int64_t)n + ranks - 1) / ranks + 3) / 4 * 4);
-    const int c0 = (int)min((int64_t)n, (int64_t)rank * run), c1 = min(n, c0 + run);
-    int held = -1;                                   // first slot of the tile in shared memory
-    // The weights of a tile to shared memory, by bulk copies where they are aligned: all its bytes are on their way at
-    // once, and no register waits for them.
-    auto bring = [&](int c, int m) {
-        const int bulk = vec ? m / 4 * 4 : 0;
+    uint32_t prefix = 0, left = q.need;
+    bool late = false;
+    if (q.need) {
+        // weights by bulk copies where they are aligned: all bytes on their way at once, and no register waits for them
+        const int bulk = (uintptr_t)acc % 16 == 0 ? n / 4 * 4 : 0;
         asm volatile("fence.proxy.async;" ::: "memory");
-        __syncthreads();                             // the tile before is no longer read
-        if (bulk) {
-            const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&sm.bar);
-            if (tid == 0) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(4 * bulk) : "memory");
-                for (int i = 0; i < bulk; i += 4096)
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                     (uint32_t)__cvta_generic_to_shared(sm.key + i)),
-                                 "l"(acc + c + i), "r"(4 * min(4096, bulk - i)), "r"(bar)
-                                 : "memory");
-            }
-            bool done = false;
-            for (int i = 0; i < (1 << 22) && !done; i++) {       // bounded
-                uint32_t ok;
-                asm volatile(
-                    "{\n.reg .pred p;\n"
-                    "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                    "selp.u32 %0, 1, 0, p;\n}\n"
-                    : "=r"(ok)
-                    : "r"(bar), "r"(phase)
-                    : "memory");
-                done = ok;
-            }
-            if (!done) late = true;
-            phase ^= 1u;
+        __syncthreads();
+        if (bulk && tid == 0) {
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(4 * bulk) : "memory");
+            for (int i = 0; i < bulk; i += 4096)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(sm.key + i)),
+                             "l"(acc + i), "r"(4 * min(4096, bulk - i)), "r"(bar)
+                             : "memory");
         }
-        for (int i = bulk + tid; i < m; i += kQeThreads) sm.key[i] = __float_as_uint(acc[c + i]);
-        if (bulk < m) __syncthreads();
-    };
-    // 4 keys at slot i of the tile in shared memory; `fresh`: still weights
-    auto keys = [&](uint32_t k[4], int i, bool fresh) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(sm.key + i);
-        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
-        if (fresh) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) k[e] = weight_key(__uint_as_float(k[e]));
-            *reinterpret_cast<uint4 *>(sm.key + i) = make_uint4(k[0], k[1], k[2], k[3]);
+        for (int i = bulk + tid; i < n; i += kQeThreads) sm.key[i] = __float_as_uint(acc[i]);
+        bool done = !bulk;
+        for (int i = 0; i < (1 << 22) && !done; i++) {           // bounded
+            uint32_t ok;
+            asm volatile(
+                "{\n.reg .pred p;\n"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n"
+                "selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(ok)
+                : "r"(bar)
+                : "memory");
+            done = ok;
         }
-    };
-
-    // threshold key: the need-th largest of the contested; left: how many of those equal to it stay
-    uint32_t prefix = 0, left = need;
-    if (need) {
+        late = !done;
 #pragma unroll 1
         for (int d = 0; d < 3; d++) {
-            const int shift = d == 0 ? 21 : d == 1 ? 11 : 0, bins = d == 1 ? kQeBins / 2 : kQeBins;
-            const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffff800u;
-            for (int i = tid; i < bins; i += kQeThreads) sm.hist[i] = 0;
+            const Digit g = digit_of(d);
+            for (int i = tid; i < g.bins; i += kQeThreads) sm.hist[i] = 0;
             __syncthreads();
-            for (int c = c0; c < c1; c += kQeTile) {
-                const int m = min(kQeTile, c1 - c), first = lo - c, end = min(m, hi - c);
-                const bool fresh = held != c;
-                if (fresh) bring(c, m);
 #pragma unroll 4
-                for (int i = 4 * tid; i < m; i += 4 * kQeThreads) {
-                    uint32_t k[4];
-                    keys(k, i, fresh);
-                    auto count = [&](int e) { atomicAdd(&sm.hist[(k[e] >> shift) & (bins - 1)], 1u); };
-                    if (i >= first && i + 4 <= end) {
-                        if (d == 0) {
+            for (int i = 4 * tid; i < n; i += 4 * kQeThreads) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(sm.key + i);
+                uint32_t k[4] = {v.x, v.y, v.z, v.w};
+                if (d == 0) {
 #pragma unroll
-                            for (int e = 0; e < 4; e++) count(e);
-                            continue;
-                        }
-                        bool any = false;            // few agree with the digits before
-#pragma unroll
-                        for (int e = 0; e < 4; e++) any |= (k[e] & above) == prefix;
-                        if (!any) continue;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (i + e >= first && i + e < end && (k[e] & above) == prefix) count(e);
+                    for (int e = 0; e < 4; e++) k[e] = weight_key(__uint_as_float(k[e]));
+                    *reinterpret_cast<uint4 *>(sm.key + i) = make_uint4(k[0], k[1], k[2], k[3]);
                 }
-                held = c;
-            }
-            sync();
-            if (!ALONE) {                // each CTA joins the counts of its share of the bins and gives all the sums
-                const int share = bins / ranks;
-                for (int i = tid; i < share; i += kQeThreads) {
-                    uint32_t x[kQeMaxCluster], v = 0;
+                bool any = d == 0;                               // few agree with the digits before
 #pragma unroll
-                    for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist, w)[rank * share + i] : 0u;
+                for (int e = 0; e < 4; e++) any |= (k[e] & g.above) == prefix;
+                if (!any) continue;
 #pragma unroll
-                    for (int w = 0; w < kQeMaxCluster; w++) v += x[w];
-#pragma unroll
-                    for (int w = 0; w < kQeMaxCluster; w++)
-                        if (w < ranks) cluster.map_shared_rank(sm.sums, w)[rank * share + i] = v;
-                }
-                cluster.sync();
-            }
-            const uint32_t *sums = ALONE ? sm.hist : sm.sums;
-            // thread t has bins [per t, per (t + 1))
-            const int per = bins / kQeThreads;
-            uint32_t mine[4] = {0, 0, 0, 0}, total = 0;
-            for (int e = 0; e < per; e++) mine[e] = sums[per * tid + e];
-            total = mine[0] + mine[1] + mine[2] + mine[3];
-            uint32_t sum;
-            uint32_t over = block_excl_scan<kQeThreads>(total, sm.ws, &sum);
-            over = sum - over - total;               // keys in the bins above the thread's
-#pragma unroll
-            for (int e = 3; e >= 0; e--) {
-                if (over < left && over + mine[e] >= left) {
-                    sm.digit = per * tid + e;
-                    sm.left = left - over;
-                }
-                over += mine[e];
+                for (int e = 0; e < 4; e++)
+                    if (i + e >= q.lo && i + e < q.hi && (k[e] & g.above) == prefix)
+                        atomicAdd(&sm.hist[(k[e] >> g.shift) & (g.bins - 1)], 1u);
             }
             __syncthreads();
-            prefix |= sm.digit << shift;
+            find_digit<kQeThreads>(sm.hist, g.bins, sm.ws, left, &sm.digit, &sm.left);
+            prefix |= sm.digit << g.shift;
             left = sm.left;
             __syncthreads();
         }
     }
-    // marks of a tile
-    auto mark = [&](int c) {
-        const int m = min(kQeTile, c1 - c), first = lo - c, end = hi - c;
-        const bool fresh = held != c;
-        if (need && fresh) bring(c, m);
-        else __syncthreads();                        // the marks are no longer read
-#pragma unroll 4
-        for (int i = 4 * tid; i < m; i += 4 * kQeThreads) {
-            uint32_t keep = 0, tie = 0;
-            if (i < end && i + 4 > first && need) {
-                uint32_t k[4];
-                keys(k, i, fresh);
+    for (int i = 4 * tid; i < n; i += 4 * kQeThreads) {
+        uint32_t keep = 0, tie = 0;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    keep |= (uint32_t)(k[e] > prefix) << e;
-                    tie |= (uint32_t)(k[e] == prefix) << e;
-                }
-            }
-            if (i < first || i + 4 > end || i + 4 > m) {         // slots that stay whatever their weight, or are none
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int j = i + e;
-                    if (j < m && j >= first && j < end) continue;
-                    keep = (keep & ~(1u << e)) | (uint32_t)(j < m) << e;
-                    tie &= ~(1u << e);
-                }
-            }
-            reinterpret_cast<uint8_t *>(sm.sums)[i >> 2] = (uint8_t)(keep | tie << 4);
+        for (int e = 0; e < 4; e++) {
+            const int j = i + e;
+            if (j >= n) continue;
+            const bool in = j >= q.lo && j < q.hi;
+            const uint32_t k = in && q.need ? sm.key[j] : 0u;
+            keep |= (uint32_t)(!in || (q.need && k > prefix)) << e;
+            tie |= (uint32_t)(in && q.need && k == prefix) << e;
         }
-        if (need) held = c;
-        __syncthreads();
-    };
-    // keep and tie bits of the thread's 32 slots of a tile
-    auto marked = [&](int c, uint32_t *keep, uint32_t *tie) {
-        uint2 w = make_uint2(0, 0);
-        const int m = min(kQeTile, c1 - c);
-        if (32 * tid < m) w = reinterpret_cast<const uint2 *>(sm.sums)[tid];
-        auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
-        *keep = nibbles(w.x) | nibbles(w.y) << 16;
-        *tie = nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16;
-        const uint32_t there = 32 * tid + 32 <= m ? 0xffffffffu : 32 * tid < m ? (1u << (m & 31)) - 1 : 0u;   // marks behind the last slot are old
-        *keep &= there;
-        *tie &= there;
-    };
-    const bool one = c1 - c0 <= kQeTile;             // one tile: marked once
+        sm.marks[i >> 2] = (uint8_t)(keep | tie << 4);
+    }
+    __syncthreads();
+    // the thread's 32 slots
+    uint2 w = make_uint2(0, 0);
+    if (32 * tid < n) w = reinterpret_cast<const uint2 *>(sm.marks)[tid];
+    auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
+    const uint32_t there = 32 * tid + 32 <= n ? 0xffffffffu : 32 * tid < n ? (1u << (n & 31)) - 1 : 0u;   // no marks behind
+    uint32_t keep = (nibbles(w.x) | nibbles(w.y) << 16) & there, total;
+    uint32_t tie = (nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16) & there;
+    // slots that stay in any case (upper half) and ties before the thread's; ties that stay are the lowest
+    const uint32_t scan = block_excl_scan<kQeThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
+    uint32_t rest = scan & 0xffffu, at = (scan >> 16) + min(rest, left);
+    const int kept = (int)((total >> 16) + min(total & 0xffffu, left));
+    for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
+    for (; keep; keep &= keep - 1) sm.list[at++] = (uint16_t)(32 * tid + __ffs(keep) - 1);
+    __syncthreads();
+    const int share = (kept + (int)gridDim.x - 1) / (int)gridDim.x, j0 = min(kept, (int)blockIdx.x * share), j1 = min(kept, j0 + share);
+    for (int j = j0 + 32 * warp; j < j1; j += kQeThreads) {
+        const int m = min(32, j1 - j);
+        move_rows(a, p, lane < m ? (int)sm.list[j + lane] : 0, m, j, true);
+    }
+    finish(a, p, n, kQeThreads);
+    if (late && tid == 0 && a.src.status && atomicCAS(a.src.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.src.status[1] = p;
+}
 
-    // kept and tied slots of this CTA, and of those before it
+// where a long pair's kept slots are listed: null where the select kernel moves the rows
+__device__ __forceinline__ int *kept_list(const QuantEvictArgs &a, int p)
+{
+    return a.keep ? a.keep + p * a.budget : a.dst.acc ? reinterpret_cast<int *>(a.dst.acc + p * a.dst.n_cap) : nullptr;
+}
+
+__global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a)
+{
+    __shared__ QsSmem sm;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    pdl_wait();
+    const Contest q = contest(a, p);
+    const float *acc = a.src.acc + (int64_t)p * a.src.n_cap;
+    const bool vec = (uintptr_t)acc % 16 == 0;       // n_cap is a multiple of 32: the same for every pair
+    const int run = (int)((((int64_t)q.n + ranks - 1) / ranks + 3) / 4 * 4);
+    const int c0 = (int)min((int64_t)q.n, (int64_t)rank * run), c1 = min(q.n, c0 + run);
+    // keys of slots i .. i + 3 (behind c1: 0)
+    auto keys = [&](uint32_t k[4], int i) {
+        if (vec && i + 4 <= c1) {
+            const float4 v = *reinterpret_cast<const float4 *>(acc + i);
+            k[0] = weight_key(v.x), k[1] = weight_key(v.y), k[2] = weight_key(v.z), k[3] = weight_key(v.w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) k[e] = i + e < c1 ? weight_key(acc[i + e]) : 0u;
+        }
+    };
+
+    // threshold key, and how many of the keys equal to it stay; own: this CTA's contested keys above it
+    uint32_t prefix = 0, left = q.need, own = 0, ties = 0;
+    if (q.need) {
+#pragma unroll 1
+        for (int d = 0; d < 3; d++) {
+            const Digit g = digit_of(d);
+            for (int i = tid; i < g.bins; i += kQsThreads) sm.hist[i] = 0;
+            __syncthreads();
+            // the contested part of the run, from a multiple of 4 on
+            const int first = max(c0, q.lo), end = min(c1, q.hi);
+#pragma unroll 4
+            for (int i = first / 4 * 4 + 4 * tid; i < end; i += 4 * kQsThreads) {
+                uint32_t k[4];
+                keys(k, i);
+                bool any = d == 0;                               // few agree with the digits before
+#pragma unroll
+                for (int e = 0; e < 4; e++) any |= (k[e] & g.above) == prefix;
+                if (!any) continue;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (i + e >= first && i + e < end && (k[e] & g.above) == prefix)
+                        atomicAdd(&sm.hist[(k[e] >> g.shift) & (g.bins - 1)], 1u);
+            }
+            cluster.sync();
+            // each CTA joins the counts of its share of the bins and gives all the sums
+            const int share = g.bins / ranks;
+            for (int i = tid; i < share; i += kQsThreads) {
+                uint32_t x[kQeMaxCluster], v = 0;
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist, w)[rank * share + i] : 0u;
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++) v += x[w];
+#pragma unroll
+                for (int w = 0; w < kQeMaxCluster; w++)
+                    if (w < ranks) cluster.map_shared_rank(sm.sums, w)[rank * share + i] = v;
+            }
+            cluster.sync();
+            find_digit<kQsThreads>(sm.sums, g.bins, sm.ws, left, &sm.digit, &sm.left);
+            const uint32_t digit = sm.digit;
+            prefix |= digit << g.shift;
+            left = sm.left;
+            for (int i = tid; i < g.bins; i += kQsThreads)
+                if (i > (int)digit) own += sm.hist[i];
+            if (d == 2) ties = sm.hist[digit];
+            __syncthreads();
+        }
+    }
+    // kept slots before this CTA's
     uint32_t before = 0, ties_before = 0;
-    if (!ALONE) {
-        uint32_t kept = 0, ties = 0;
-        for (int c = c0; c < c1; c += kQeTile) {
-            uint32_t keep, tie;
-            mark(c);
-            marked(c, &keep, &tie);
-            kept += __popc(keep);
-            ties += __popc(tie);
+    {
+        own = __reduce_add_sync(kFull, own);
+        if (tid == 0) {
+            sm.count[0] = (uint32_t)(c1 - c0 - max(0, min(c1, q.hi) - max(c0, q.lo)));       // not contested
+            sm.count[1] = ties;
         }
-        if (tid < 2) sm.count[tid] = 0;
         __syncthreads();
-        kept = __reduce_add_sync(kFull, kept);
-        ties = __reduce_add_sync(kFull, ties);
-        if (lane == 0) {
-            atomicAdd(&sm.count[0], kept);
-            atomicAdd(&sm.count[1], ties);
-        }
+        if (lane == 0) atomicAdd(&sm.count[0], own);
         cluster.sync();
         for (int w = 0; w < rank; w++) {
             const uint32_t *o = cluster.map_shared_rank(sm.count, w);
@@ -321,34 +371,56 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         before += min(ties_before, left);            // ties that stay are the lowest
         cluster.barrier_arrive();                    // the other CTAs' memory has been read
     }
-    for (int c = c0; c < c1; c += kQeTile) {
-        if (ALONE || !one) mark(c);
-        uint32_t keep, tie, total;
-        marked(c, &keep, &tie);
-        // slots that stay in any case (upper half) and ties before the thread's
-        const uint32_t scan = block_excl_scan<kQeThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
+    int *list = kept_list(a, p);
+    for (int c = c0; c < c1; c += kQsChunk) {
+        uint32_t keep = 0, tie = 0, total;           // of the thread's slots i0 ..
+        const int i0 = c + kQsPer * tid;
+#pragma unroll
+        for (int h = 0; h < kQsPer; h += 4) {
+            const int i = i0 + h;
+            uint32_t k[4] = {0u, 0u, 0u, 0u};
+            if (q.need && i < c1) keys(k, i);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int j = i + e;
+                if (j >= c1) continue;
+                const bool in = j >= q.lo && j < q.hi;
+                keep |= (uint32_t)(!in || (q.need && k[e] > prefix)) << (h + e);
+                tie |= (uint32_t)(in && q.need && k[e] == prefix) << (h + e);
+            }
+        }
+        const uint32_t scan = block_excl_scan<kQsThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
         uint32_t rest = ties_before + (scan & 0xffffu), at = (scan >> 16) + min(rest, left) - min(ties_before, left);
-        const int moved = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));
+        const int kept = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));
         ties_before += total & 0xffffu;
         for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
-        for (; keep; keep &= keep - 1) sm.list[at++] = (uint16_t)(32 * tid + __ffs(keep) - 1);
-        __syncthreads();
-        if (ALONE) {                     // each of the pair's CTAs moves a share
-            const int share = (moved + gridDim.x - 1) / gridDim.x, j = min(moved, (int)blockIdx.x * share);
-            move_rows(a, p, c, sm.list + j, min(share, moved - j), before + j);
-        } else {
-            move_rows(a, p, c, sm.list, moved, before);
+        int *to = list ? list + before : sm.list;
+        for (; keep; keep &= keep - 1) to[at++] = i0 + __ffs(keep) - 1;
+        if (!list) {
+            __syncthreads();
+            for (int j = 32 * warp; j < kept; j += kQsThreads) {
+                const int m = min(32, kept - j);
+                move_rows(a, p, lane < m ? sm.list[j + lane] : 0, m, before + j, false);
+            }
+            __syncthreads();
         }
-        before += moved;
-        __syncthreads();
+        before += kept;
     }
-    const int64_t kept = all ? n : a.budget;
-    if (a.keep)
-        for (int64_t o = kept + (int)blockIdx.x * kQeThreads + tid; o < a.budget; o += (int64_t)gridDim.x * kQeThreads)
-            a.keep[p * a.budget + o] = -1;
-    if (blockIdx.x == 0 && tid == 0) a.dst.lens[p] = (int32_t)kept;
-    if (late && tid == 0 && a.src.status && atomicCAS(a.src.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.src.status[1] = p;
-    if (!ALONE) cluster.barrier_wait();              // and this CTA's by the others
+    finish(a, p, q.n, kQsThreads);
+    cluster.barrier_wait();                          // and this CTA's by the others
+}
+
+// Rows of the listed slots, a warp 32 of them.
+__global__ void __launch_bounds__(kQsThreads) k_quant_gather(QuantEvictArgs a)
+{
+    const int p = blockIdx.y, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int kept = (int)min((int64_t)quant_len(a.src, p), a.budget);
+    const int *list = kept_list(a, p);
+    const int64_t j = (int64_t)blockIdx.x * kQsThreads + (threadIdx.x & ~31);
+    if (j >= kept) return;
+    const int m = min(32, kept - (int)j);
+    move_rows(a, p, lane < m ? list[j + lane] : 0, m, j, false);
 }
 
 cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
@@ -357,21 +429,20 @@ cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> done[2][kMaxDevices];
-    const bool alone = a.src.n_cap <= kQeTile;
-    auto kern = alone ? k_quant_evict<true> : k_quant_evict<false>;
-    e = dyn_smem_limit(kern, (int)sizeof(QeSmem), done[alone]);
-    if (e != cudaSuccess) return e;
-    // CTAs per pair: as many as hold its slots in shared memory, and more while there is room for all at once and 128
-    // slots for each
-    int c = 1;
-    while (c < kQeMaxCluster && ((!alone && a.src.n_cap > (int64_t)c * kQeTile) ||
-                                 (2 * c * a.src.bh <= 2 * sms && a.src.n_cap >= 2 * c * 128)))
-        c *= 2;
+    int c = 1;                           // CTAs per pair
+    if (a.src.n_cap <= kQeTile) {
+        static std::atomic<int> done[kMaxDevices];
+        e = dyn_smem_limit(k_quant_evict, (int)sizeof(QeSmem), done);
+        if (e != cudaSuccess) return e;
+        // more while there is room for all at once and 128 slots for each
+        while (c < 8 && 2 * c * a.src.bh <= 2 * sms && a.src.n_cap >= 2 * c * 128) c *= 2;
+        return launch_pdl(k_quant_evict, dim3(c, a.src.bh), dim3(kQeThreads), sizeof(QeSmem), s, a);
+    }
+    // more while there is room for all at once and four slots for each thread
+    while (c < kQeMaxCluster && 2 * c * a.src.bh <= 4 * sms && a.src.n_cap >= 2 * c * 4 * kQsThreads) c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c, a.src.bh);
-    cfg.blockDim = dim3(kQeThreads);
-    cfg.dynamicSmemBytes = sizeof(QeSmem);
+    cfg.blockDim = dim3(kQsThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -380,9 +451,12 @@ cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = alone ? attr + 1 : attr;
-    cfg.numAttrs = alone ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_quant_select, a);
+    if (e != cudaSuccess || !(a.keep || a.dst.acc)) return e;
+    const int64_t most = a.budget < a.src.n_cap ? a.budget : a.src.n_cap;
+    return launch_pdl(k_quant_gather, dim3((unsigned)((most + kQsThreads - 1) / kQsThreads), a.src.bh), dim3(kQsThreads), 0, s, a);
 }
 
 }  // namespace pk
