@@ -46,14 +46,15 @@ struct QeSmem {
 };
 static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots");
 
+constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (66 us for 50)
 struct QsSmem {
-    uint32_t hist[kQeBins];              // this CTA's counts
+    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts
     uint32_t sums[kQeBins];              // all CTAs' counts
     uint32_t ws[kQsThreads / 32 + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
-    int list[kQsChunk];                  // kept slots of a chunk, when this kernel moves the rows
 };
+static_assert(kQsChunk * sizeof(int) <= 2 * kQeBins * sizeof(uint32_t), "a chunk's list takes the place of the first two copies");
 
 // digit d of the select: its place, its bins, and the bits above it
 struct Digit {
@@ -70,6 +71,9 @@ __device__ __forceinline__ uint32_t weight_key(float x)
 {
     return x != x ? 0u : ord_f32(x + 0.0f);
 }
+
+// The weight of a key (not NaN's).
+__device__ __forceinline__ float key_weight(uint32_t k) { return unord_f32(k); }
 
 // The bin of the left-th largest key by the counts `sums`: *digit, and in *left
 // its rank within the bin; over a CTA of NT threads.
@@ -294,14 +298,14 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
     const bool vec = (uintptr_t)acc % 16 == 0;       // n_cap is a multiple of 32: the same for every pair
     const int run = (int)((((int64_t)q.n + ranks - 1) / ranks + 3) / 4 * 4);
     const int c0 = (int)min((int64_t)q.n, (int64_t)rank * run), c1 = min(q.n, c0 + run);
-    // keys of slots i .. i + 3 (behind c1: 0)
-    auto keys = [&](uint32_t k[4], int i) {
+    // weights of slots i .. i + 3 (behind c1: NaN)
+    auto weights = [&](float x[4], int i) {
         if (vec && i + 4 <= c1) {
             const float4 v = *reinterpret_cast<const float4 *>(acc + i);
-            k[0] = weight_key(v.x), k[1] = weight_key(v.y), k[2] = weight_key(v.z), k[3] = weight_key(v.w);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; e++) k[e] = i + e < c1 ? weight_key(acc[i + e]) : 0u;
+            for (int e = 0; e < 4; e++) x[e] = i + e < c1 ? acc[i + e] : __uint_as_float(0x7fffffffu);
         }
     };
 
@@ -311,22 +315,53 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
 #pragma unroll 1
         for (int d = 0; d < 3; d++) {
             const Digit g = digit_of(d);
-            for (int i = tid; i < g.bins; i += kQsThreads) sm.hist[i] = 0;
+            const int copies = d == 0 ? kQsCopies : 1;
+            for (int i = tid; i < copies * kQeBins; i += kQsThreads) sm.hist[0][i] = 0;
             __syncthreads();
             // the contested part of the run, from a multiple of 4 on
             const int first = max(c0, q.lo), end = min(c1, q.hi);
-#pragma unroll 4
-            for (int i = first / 4 * 4 + 4 * tid; i < end; i += 4 * kQsThreads) {
-                uint32_t k[4];
-                keys(k, i);
-                bool any = d == 0;                               // few agree with the digits before
+            // keys that agree with the digits before are a range of weights (the first digit 0: NaN alone)
+            const bool nan = d > 0 && (prefix >> 21) == 0;
+            const float low = d == 0 || nan ? 0.0f : key_weight(max(prefix, 0x007fffffu));                 // -inf
+            const float high = d == 0 || nan ? 0.0f : key_weight(min(prefix | ~g.above, 0xff800000u));      // inf
+            uint32_t *hist = sm.hist[d == 0 ? lane & (kQsCopies - 1) : 0];
+            auto count = [&](const float x[4], int i) {
+                if (d > 0 && !nan) {                 // few
+                    bool any = false;
 #pragma unroll
-                for (int e = 0; e < 4; e++) any |= (k[e] & g.above) == prefix;
-                if (!any) continue;
+                    for (int e = 0; e < 4; e++) any |= x[e] >= low && x[e] <= high;
+                    if (!any) return;
+                }
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (i + e >= first && i + e < end && (k[e] & g.above) == prefix)
-                        atomicAdd(&sm.hist[(k[e] >> g.shift) & (g.bins - 1)], 1u);
+                for (int e = 0; e < 4; e++) {
+                    const uint32_t k = weight_key(x[e]);
+                    if (i + e >= first && i + e < end && (k & g.above) == prefix) atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
+                }
+            };
+            int i = first / 4 * 4 + 4 * tid;
+            for (; vec && i + 12 * kQsThreads + 4 <= c1 && i < end; i += 16 * kQsThreads) {      // 4 loads in flight
+                float4 v[4];
+#pragma unroll
+                for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
+#pragma unroll
+                for (int h = 0; h < 4; h++) {
+                    const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                    count(x, i + 4 * h * kQsThreads);
+                }
+            }
+            for (; i < end; i += 4 * kQsThreads) {
+                float x[4];
+                weights(x, i);
+                count(x, i);
+            }
+            if (d == 0) {
+                __syncthreads();
+                for (int i = tid; i < kQeBins; i += kQsThreads) {
+                    uint32_t v = 0;
+#pragma unroll
+                    for (int w = 0; w < kQsCopies; w++) v += sm.hist[w][i];
+                    sm.hist[0][i] = v;
+                }
             }
             cluster.sync();
             // each CTA joins the counts of its share of the bins and gives all the sums
@@ -334,7 +369,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             for (int i = tid; i < share; i += kQsThreads) {
                 uint32_t x[kQeMaxCluster], v = 0;
 #pragma unroll
-                for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist, w)[rank * share + i] : 0u;
+                for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist[0], w)[rank * share + i] : 0u;
 #pragma unroll
                 for (int w = 0; w < kQeMaxCluster; w++) v += x[w];
 #pragma unroll
@@ -347,8 +382,8 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             prefix |= digit << g.shift;
             left = sm.left;
             for (int i = tid; i < g.bins; i += kQsThreads)
-                if (i > (int)digit) own += sm.hist[i];
-            if (d == 2) ties = sm.hist[digit];
+                if (i > (int)digit) own += sm.hist[0][i];
+            if (d == 2) ties = sm.hist[0][digit];
             __syncthreads();
         }
     }
@@ -371,36 +406,43 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         before += min(ties_before, left);            // ties that stay are the lowest
         cluster.barrier_arrive();                    // the other CTAs' memory has been read
     }
-    int *list = kept_list(a, p);
+    int *list = kept_list(a, p), *chunk = reinterpret_cast<int *>(sm.hist);
+    const bool nan = prefix == 0;                    // the threshold is NaN: all others are above it
+    const float limit = nan ? 0.0f : key_weight(prefix);
     for (int c = c0; c < c1; c += kQsChunk) {
         uint32_t keep = 0, tie = 0, total;           // of the thread's slots i0 ..
         const int i0 = c + kQsPer * tid;
+        float x[kQsPer];
+        if (vec && i0 + kQsPer <= c1) {              // all loads in flight
 #pragma unroll
-        for (int h = 0; h < kQsPer; h += 4) {
-            const int i = i0 + h;
-            uint32_t k[4] = {0u, 0u, 0u, 0u};
-            if (q.need && i < c1) keys(k, i);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int j = i + e;
-                if (j >= c1) continue;
-                const bool in = j >= q.lo && j < q.hi;
-                keep |= (uint32_t)(!in || (q.need && k[e] > prefix)) << (h + e);
-                tie |= (uint32_t)(in && q.need && k[e] == prefix) << (h + e);
+            for (int h = 0; h < kQsPer; h += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(acc + i0 + h);
+                x[h] = v.x, x[h + 1] = v.y, x[h + 2] = v.z, x[h + 3] = v.w;
             }
+        } else {
+#pragma unroll
+            for (int h = 0; h < kQsPer; h++) x[h] = i0 + h < c1 ? acc[i0 + h] : 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < kQsPer; h++) {
+            const int j = i0 + h;
+            const bool in = j >= q.lo && j < q.hi, above = nan ? x[h] == x[h] : x[h] > limit, equal = nan ? x[h] != x[h] : x[h] == limit;
+            if (j >= c1) continue;
+            keep |= (uint32_t)(!in || (q.need && above)) << h;
+            tie |= (uint32_t)(in && q.need && equal) << h;
         }
         const uint32_t scan = block_excl_scan<kQsThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
         uint32_t rest = ties_before + (scan & 0xffffu), at = (scan >> 16) + min(rest, left) - min(ties_before, left);
         const int kept = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));
         ties_before += total & 0xffffu;
         for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
-        int *to = list ? list + before : sm.list;
+        int *to = list ? list + before : chunk;
         for (; keep; keep &= keep - 1) to[at++] = i0 + __ffs(keep) - 1;
         if (!list) {
             __syncthreads();
             for (int j = 32 * warp; j < kept; j += kQsThreads) {
                 const int m = min(32, kept - j);
-                move_rows(a, p, lane < m ? sm.list[j + lane] : 0, m, before + j, false);
+                move_rows(a, p, lane < m ? chunk[j + lane] : 0, m, before + j, false);
             }
             __syncthreads();
         }
