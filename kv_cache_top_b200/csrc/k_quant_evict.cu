@@ -31,8 +31,7 @@ constexpr int kQeThreads = 512;
 constexpr int kQeBins = 2048;
 constexpr int kQeTile = 16384;           // slots in shared memory: two CTAs to an SM
 constexpr int kQsThreads = 256;          // select
-constexpr int kQsPer = 16;               // consecutive slots a thread lists at once
-constexpr int kQsChunk = kQsPer * kQsThreads;
+constexpr int kQsChunk = 32 * kQsThreads;     // slots listed at once, 32 consecutive ones a thread
 constexpr int kQeMaxCluster = 8;
 
 struct QeSmem {
@@ -54,7 +53,7 @@ struct QsSmem {
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
 };
-static_assert(kQsChunk * sizeof(int) <= 2 * kQeBins * sizeof(uint32_t), "a chunk's list takes the place of the first two copies");
+static_assert(kQsChunk * 2 <= 2 * kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4, "a chunk's list and marks take the place of the copies");
 
 // digit d of the select: its place, its bins, and the bits above it
 struct Digit {
@@ -160,6 +159,17 @@ __device__ __forceinline__ Contest contest(const QuantEvictArgs &a, int p)
     return Contest{n, (int)a.sink, n - (int)a.recent, (uint32_t)(a.budget - a.sink - a.recent)};
 }
 
+// Marks of 4 slots a byte, bits 0..3 those that stay and 4..7 those that tie:
+// the bits of a thread's 32 slots, of which the first `there` are.
+__device__ __forceinline__ void marked(const uint8_t *marks, int there, uint32_t *keep, uint32_t *tie)
+{
+    const uint2 w = *reinterpret_cast<const uint2 *>(marks);
+    auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
+    const uint32_t mask = there >= 32 ? 0xffffffffu : there > 0 ? (1u << there) - 1 : 0u;       // marks behind are old
+    *keep = (nibbles(w.x) | nibbles(w.y) << 16) & mask;
+    *tie = (nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16) & mask;
+}
+
 // What is the same in both ways: the length, the end of the list, the check.
 __device__ __forceinline__ void finish(const QuantEvictArgs &a, int p, int n, int threads)
 {
@@ -257,13 +267,8 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         sm.marks[i >> 2] = (uint8_t)(keep | tie << 4);
     }
     __syncthreads();
-    // the thread's 32 slots
-    uint2 w = make_uint2(0, 0);
-    if (32 * tid < n) w = reinterpret_cast<const uint2 *>(sm.marks)[tid];
-    auto nibbles = [](uint32_t x) { x &= 0x0f0f0f0fu; x = (x | x >> 4) & 0x00ff00ffu; return (x | x >> 8) & 0xffffu; };
-    const uint32_t there = 32 * tid + 32 <= n ? 0xffffffffu : 32 * tid < n ? (1u << (n & 31)) - 1 : 0u;   // no marks behind
-    uint32_t keep = (nibbles(w.x) | nibbles(w.y) << 16) & there, total;
-    uint32_t tie = (nibbles(w.x >> 4) | nibbles(w.y >> 4) << 16) & there;
+    uint32_t keep, tie, total;
+    marked(sm.marks + 8 * tid, n - 32 * tid, &keep, &tie);
     // slots that stay in any case (upper half) and ties before the thread's; ties that stay are the lowest
     const uint32_t scan = block_excl_scan<kQeThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
     uint32_t rest = scan & 0xffffu, at = (scan >> 16) + min(rest, left);
@@ -406,46 +411,60 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         before += min(ties_before, left);            // ties that stay are the lowest
         cluster.barrier_arrive();                    // the other CTAs' memory has been read
     }
-    int *list = kept_list(a, p), *chunk = reinterpret_cast<int *>(sm.hist);
+    int *list = kept_list(a, p);
+    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.hist[0]);
+    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[2]);
     const bool nan = prefix == 0;                    // the threshold is NaN: all others are above it
     const float limit = nan ? 0.0f : key_weight(prefix);
     for (int c = c0; c < c1; c += kQsChunk) {
-        uint32_t keep = 0, tie = 0, total;           // of the thread's slots i0 ..
-        const int i0 = c + kQsPer * tid;
-        float x[kQsPer];
-        if (vec && i0 + kQsPer <= c1) {              // all loads in flight
+        auto mark = [&](const float x[4], int i) {
+            uint32_t keep = 0, tie = 0;
 #pragma unroll
-            for (int h = 0; h < kQsPer; h += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(acc + i0 + h);
-                x[h] = v.x, x[h + 1] = v.y, x[h + 2] = v.z, x[h + 3] = v.w;
+            for (int e = 0; e < 4; e++) {
+                const bool in = i + e >= q.lo && i + e < q.hi;
+                const bool above = nan ? x[e] == x[e] : x[e] > limit, equal = nan ? x[e] != x[e] : x[e] == limit;
+                keep |= (uint32_t)(!in || (q.need && above)) << e;
+                tie |= (uint32_t)(in && q.need && equal) << e;
             }
-        } else {
+            marks[(i - c) >> 2] = (uint8_t)(keep | tie << 4);
+        };
+        const int stop = min(c1, c + kQsChunk);
+        int i = c + 4 * tid;
+        for (; vec && i + 12 * kQsThreads + 4 <= stop; i += 16 * kQsThreads) {       // 4 loads in flight
+            float4 v[4];
 #pragma unroll
-            for (int h = 0; h < kQsPer; h++) x[h] = i0 + h < c1 ? acc[i0 + h] : 0.0f;
-        }
+            for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
 #pragma unroll
-        for (int h = 0; h < kQsPer; h++) {
-            const int j = i0 + h;
-            const bool in = j >= q.lo && j < q.hi, above = nan ? x[h] == x[h] : x[h] > limit, equal = nan ? x[h] != x[h] : x[h] == limit;
-            if (j >= c1) continue;
-            keep |= (uint32_t)(!in || (q.need && above)) << h;
-            tie |= (uint32_t)(in && q.need && equal) << h;
+            for (int h = 0; h < 4; h++) {
+                const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                mark(x, i + 4 * h * kQsThreads);
+            }
         }
+        for (; i < stop; i += 4 * kQsThreads) {
+            float x[4];
+            weights(x, i);
+            mark(x, i);
+        }
+        __syncthreads();
+        uint32_t keep, tie, total;
+        const int i0 = c + 32 * tid;
+        marked(marks + 8 * tid, stop - i0, &keep, &tie);
         const uint32_t scan = block_excl_scan<kQsThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
         uint32_t rest = ties_before + (scan & 0xffffu), at = (scan >> 16) + min(rest, left) - min(ties_before, left);
         const int kept = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));
         ties_before += total & 0xffffu;
         for (; tie && rest < left; tie &= tie - 1, rest++) keep |= tie & -tie;
-        int *to = list ? list + before : chunk;
-        for (; keep; keep &= keep - 1) to[at++] = i0 + __ffs(keep) - 1;
-        if (!list) {
+        if (list) {
+            for (; keep; keep &= keep - 1) list[before + at++] = i0 + __ffs(keep) - 1;
+        } else {
+            for (; keep; keep &= keep - 1) chunk[at++] = (uint16_t)(32 * tid + __ffs(keep) - 1);
             __syncthreads();
             for (int j = 32 * warp; j < kept; j += kQsThreads) {
                 const int m = min(32, kept - j);
-                move_rows(a, p, lane < m ? chunk[j + lane] : 0, m, before + j, false);
+                move_rows(a, p, lane < m ? c + chunk[j + lane] : 0, m, before + j, false);
             }
-            __syncthreads();
         }
+        __syncthreads();                             // the marks and the list have been read
         before += kept;
     }
     finish(a, p, q.n, kQsThreads);
