@@ -14,8 +14,9 @@ namespace pk {
 constexpr int kQaWarps = 16;
 constexpr int kQaThreads = 32 * kQaWarps;
 constexpr int kQaStages = 2;             // blocks in flight per warp
-constexpr int kQaMinShare = 8;           // blocks a worker takes at least: two warps for each of an SM's schedulers
-constexpr int kQaPer = 5;                // pairs a lane plans
+constexpr int kQaFew = 4;                // warps of a small worker
+constexpr int kQaGroups = kQaWarps / kQaFew;
+constexpr int kQaManyPairs = 129;        // pairs from which on workers are small (256 of 577 keys: 21 us for 22; 64 ragged ones: 37 for 35)
 constexpr int kQaCol = kD + 4;           // floats between the columns of a warp's sums in shared memory
 constexpr int kQmThreads = 256;          // merge kernel
 constexpr int kQmKeys = 2048;            // keys of a merge CTA's part of acc
@@ -28,70 +29,76 @@ struct QaSmem {
     float4 vs[kQaWarps][kQKeys];         // ... and V
     float size[kQaWarps][kQKeys];        // exponent of each key's largest V scale
     float m[kQaWarps][8], l[kQaWarps][8];
-    uint32_t q[2][kMaxGroup][4][4][8];   // [segment parity][head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
-    float qscale[2][kMaxGroup];
+    float qscale[kQaGroups][2][kMaxGroup];
     uint32_t ws[kQaWarps + 1];
-    uint2 counts[kQaWarps];
     float factor[kQaWarps][8];           // of a warp's column in the segment's sums
-    uint32_t pair, first, start, end;
+    uint32_t pair[kQaGroups], first[kQaGroups], start[kQaGroups], end[kQaGroups];
     int by_pairs;
+    uint32_t share;
     int has[kQaWarps];
+    alignas(16) uint32_t q[kQaGroups][2][kMaxGroup][4][4][8];      // last: as many workers as the CTA has; [worker][segment parity][head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
 };
+static_assert(offsetof(QaSmem, bar) % 16 == 0 && offsetof(QaSmem, ks) % 16 == 0 && offsetof(QaSmem, vs) % 16 == 0 && offsetof(QaSmem, size) % 16 == 0 &&
+              offsetof(QaSmem, q) % 16 == 0, "read 8 and 16 bytes at a time");
 static_assert(8 * kQaCol * 4 <= kQBlock, "a warp's sums fit the block that it has consumed");
 
-int quant_attend_workers(int num_sms) { return min(num_sms, kQMaxWorkers); }
+// blocks a worker of `span` warps takes at least
+__host__ __device__ constexpr int min_share(int span) { return span == kQaWarps ? 8 : span; }
 
 __device__ __forceinline__ uint32_t block_count(const QuantCache &c, int p) { return (uint32_t)(quant_len(c, p) + kQKeys - 1) / kQKeys; }
 
-// Block counts of all pairs, and of those before pair `end`, over a CTA of NT threads.
-template <int NT>
-__device__ uint2 count_blocks(const QuantCache &c, int end, uint2 *s)
+// Block count of all pairs, over the CTA.
+__device__ uint32_t count_blocks(const QuantCache &c, uint32_t *s)
 {
-    uint2 v = make_uint2(0, 0);
-    for (int p = threadIdx.x; p < c.bh; p += NT) {
-        const uint32_t n = block_count(c, p);
-        v.x += n;
-        if (p < end) v.y += n;
-    }
-    v = make_uint2(__reduce_add_sync(kFull, v.x), __reduce_add_sync(kFull, v.y));
+    uint32_t v = 0;
+    for (int p = threadIdx.x; p < c.bh; p += kQaThreads) v += block_count(c, p);
+    v = __reduce_add_sync(kFull, v);
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = make_uint2(0, 0);
+    v = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; w++) {
-        v.x += s[w].x;
-        v.y += s[w].y;
-    }
+    for (int w = 0; w < kQaWarps; w++) v += s[w];
+    __syncthreads();
     return v;
 }
 
-// Up to 32 kQaPer pairs, and no more than workers: a worker takes blocks of one
+// Up to 32 PER pairs, and no more than workers: a worker takes blocks of one
 // pair only, `share` of them, the smallest that does with the workers there
 // are, unless that is more than an even share by over a round of the warps, what
 // a second merge costs (64 ragged pairs of up to 282 blocks: 35 us by pairs, 55
 // evenly; 64 pairs of 4096 blocks, 2 workers for each and 20 idle: 300 and
 // 268).  Else the pairs' blocks are laid end to end and cut
-// evenly.  By one warp: the share, or 0 for even ones; lane l has the block
-// counts nb of pairs kQaPer l ..
-__device__ uint32_t plan_pairs(const QuantCache &c, int workers, int lane, uint32_t nb[kQaPer])
+// evenly.  By one warp: the share, or 0 for even ones; nb[i] is the block count
+// of pair lane + 32 i.
+__device__ __forceinline__ uint32_t ceil_share(uint32_t nb, uint32_t share, float inv)
 {
-    if (c.bh > 32 * kQaPer || c.bh > workers) return 0;
+    uint32_t q = (uint32_t)((float)nb * inv);        // off by one at most: at most kQMaxWorkers + the pair's round
+    int r = (int)(nb - q * share);
+    if (r < 0) q--, r += (int)share;
+    if (r >= (int)share) q++, r -= (int)share;
+    return q + (r > 0);
+}
+template <int PER>
+__device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers, int span, int lane, uint32_t nb[PER])
+{
+    if (c.bh > 32 * PER || c.bh > workers) return 0;
     uint32_t total = 0;
 #pragma unroll
-    for (int i = 0; i < kQaPer; i++) {
-        const int p = kQaPer * lane + i;
+    for (int i = 0; i < PER; i++) {
+        const int p = lane + 32 * i;
         nb[i] = p < c.bh ? block_count(c, p) : 0u;
+        total += nb[i];
     }
-#pragma unroll
-    for (int i = 0; i < kQaPer; i++) total += nb[i];
     total = __reduce_add_sync(kFull, total);
     auto need = [&](uint32_t share) {    // workers at this share
+        const float inv = 1.0f / (float)share;
         uint32_t k = 0;
 #pragma unroll
-        for (int i = 0; i < kQaPer; i++) k += (nb[i] + share - 1) / share;
+        for (int i = 0; i < PER; i++)
+            if (32 * i < c.bh) k += ceil_share(nb[i], share, inv);
         return __reduce_add_sync(kFull, k);
     };
-    uint32_t lo = (uint32_t)quant_share(total, workers, kQaMinShare), hi = lo + kQaWarps;
+    uint32_t lo = (uint32_t)quant_share(total, workers, min_share(span)), hi = lo + span;
     if (need(hi) > (uint32_t)workers) return 0;
     while (lo < hi) {
         const uint32_t mid = (lo + hi) / 2;
@@ -99,6 +106,46 @@ __device__ uint32_t plan_pairs(const QuantCache &c, int workers, int lane, uint3
         else lo = mid + 1;
     }
     return hi;
+}
+
+// By pairs: the blocks of the workers worker0 .. of a CTA, by its first warp.
+template <int PER, int SPAN>
+__device__ __forceinline__ void place_workers(const QuantCache &c, int workers, uint32_t worker0, int lane, QaSmem &sm)
+{
+    constexpr int kGroups = kQaWarps / SPAN;
+    uint32_t nb[PER];
+    const uint32_t share = plan_pairs<PER>(c, workers, SPAN, lane, nb);
+    if (lane == 0) {
+        sm.by_pairs = share > 0;
+        sm.share = share;
+    }
+    if (lane < kGroups) sm.end[lane] = 0;        // no work unless a pair has some
+    __syncwarp();
+    if (share > 0) {
+        const float inv = 1.0f / (float)share;
+        uint32_t w0 = 0, f0 = 0;                 // workers and blocks of the pairs before
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            if (32 * i >= c.bh) break;
+            const uint32_t k = ceil_share(nb[i], share, inv);
+            uint32_t w = k, f = nb[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
+                if (lane >= o) w += x, f += y;
+            }
+            const uint32_t we = w0 + w, fe = f0 + f;         // ends of the lane's pair
+            for (uint32_t i0 = max(we - k, worker0); i0 < min(we, worker0 + kGroups); i0++) {
+                const int j = i0 - worker0;
+                sm.pair[j] = lane + 32 * i;
+                sm.first[j] = fe - nb[i];
+                sm.start[j] = fe - nb[i] + (i0 - (we - k)) * share;
+                sm.end[j] = min(fe, sm.start[j] + share);
+            }
+            w0 += __shfl_sync(kFull, w, 31);
+            f0 += __shfl_sync(kFull, f, 31);
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -271,7 +318,10 @@ __device__ __forceinline__ void load_q(float v[4], const QuantAttendArgs &a, int
 // the low parts are the columns 4..7, else they are a second product.
 // The reference maximum is of logit + exponent of the key's largest value
 // scale, so that w, not p, is what stays within a half's range.
-template <bool WIDE>
+//
+// A worker is a CTA, or (SPAN) 4 warps of one: with many pairs, small workers
+// lose less to rounds that do not fill their warps, and to merges.
+template <bool WIDE, int SPAN>
 __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs a)
 {
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -283,73 +333,51 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     pdl_trigger();
 
     // this worker's blocks [x0, end) of all, and the pair of the first
-    uint32_t x0, end;
-    if (warp == 0) {
-        uint32_t nb[kQaPer], mine = 0, first = 0;
-        const uint32_t share = plan_pairs(a.c, a.workers, lane, nb);
-        if (lane == 0) {
-            sm.by_pairs = share > 0;
-            sm.end = 0;                  // no work unless a pair has some for this worker
-        }
-        __syncwarp();
-        if (share > 0) {
-#pragma unroll
-            for (int i = 0; i < kQaPer; i++) {
-                mine += (nb[i] + share - 1) / share;
-                first += nb[i];
-            }
-            uint32_t w = mine, f = first;            // workers and blocks before the lane's pairs
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
-                if (lane >= o) w += x, f += y;
-            }
-            w -= mine;
-            f -= first;
-#pragma unroll
-            for (int i = 0; i < kQaPer; i++) {
-                const uint32_t k = (nb[i] + share - 1) / share;
-                if (blockIdx.x >= w && blockIdx.x < w + k) {
-                    sm.pair = kQaPer * lane + i;
-                    sm.first = f;
-                    sm.start = f + (blockIdx.x - w) * share;
-                    sm.end = min(f + nb[i], sm.start + share);
-                }
-                w += k;
-                f += nb[i];
-            }
-        }
+    constexpr int kGroups = kQaWarps / SPAN;
+    const int group = warp / SPAN, mate = warp % SPAN;           // worker within the CTA, warp within the worker
+    const uint32_t worker0 = blockIdx.x * kGroups, worker = worker0 + group;
+    auto sync = [&]() {
+        if (SPAN == kQaWarps) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * SPAN) : "memory");
+    };
+    if (warp == 0) {                     // each row of 32 pairs that is planned costs 0.1 us
+        if (a.c.bh <= 32) place_workers<1, SPAN>(a.c, a.workers, worker0, lane, sm);
+        else place_workers<SPAN == kQaWarps ? 4 : 8, SPAN>(a.c, a.workers, worker0, lane, sm);
     }
     __syncthreads();
-    if (sm.by_pairs) {
-        x0 = sm.start;
-        end = sm.end;
-        if (end == 0) return;
-    } else {
-        const uint32_t total = count_blocks<kQaThreads>(a.c, 0, sm.counts).x;
-        const uint32_t share = (uint32_t)quant_share(total, a.workers, kQaMinShare);
-        x0 = blockIdx.x * share;
-        if (x0 >= total) return;
-        end = min(total, x0 + share);
+    if (!sm.by_pairs) {
+        const uint32_t total = count_blocks(a.c, sm.ws);
+        const uint32_t share = (uint32_t)quant_share(total, a.workers, min_share(SPAN));
+        if (worker0 * share >= total) return;
+        if (tid == 0) sm.share = share;
         for (uint32_t base = 0, c = 0;; c += kQaThreads) {
             const uint32_t v = c + tid < (uint32_t)a.c.bh ? block_count(a.c, c + tid) : 0u;
-            uint32_t sum;
+            uint32_t sum, last = 0;
             const uint32_t before = base + block_excl_scan<kQaThreads>(v, sm.ws, &sum);
-            if (x0 >= before && x0 - before < v) {
-                sm.pair = c + tid;
-                sm.first = before;
+#pragma unroll
+            for (int j = 0; j < kGroups; j++) {
+                const uint32_t x = (worker0 + j) * share;
+                if (x >= before && x - before < v) {
+                    sm.pair[j] = c + tid;
+                    sm.first[j] = before;
+                    sm.start[j] = x;
+                    sm.end[j] = min(total, x + share);
+                }
+                if (x < total) last = x;
             }
             base += sum;
-            if (base > x0) break;
+            if (base > last) break;
         }
+        __syncthreads();
     }
-    __syncthreads();
-    int p = (int)sm.pair;
-    uint32_t first = sm.first;           // first block of pair p
+    const uint32_t x0 = sm.start[group], end = sm.end[group];
+    if (end == 0) return;
+    int p = (int)sm.pair[group];
+    uint32_t first = sm.first[group];    // first block of pair p
     const int64_t pair_blocks = a.c.n_cap / kQKeys;
 
-    // the warp's blocks are x = warp (mod kQaWarps); copies run ahead of x
-    uint32_t x = x0 + (warp + kQaWarps - x0 % kQaWarps) % kQaWarps;
+    // the warp's blocks are x = mate (mod SPAN); copies run ahead of x
+    uint32_t x = x0 + (mate + SPAN - x0 % SPAN) % SPAN;
     uint32_t fx = x, ffirst = first, fnb = block_count(a.c, p);
     int fp = p;
     auto fetch = [&](int s) {
@@ -359,7 +387,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             fnb = block_count(a.c, ++fp);
         }
         if (lane == 0) fetch_block(sm.ring[warp][s], a.c.blocks + (fp * pair_blocks + (fx - ffirst)) * kQBlock, &sm.bar[warp][s]);
-        fx += kQaWarps;
+        fx += SPAN;
     };
 #pragma unroll 1
     for (int s = 0; s < kQaStages; s++) fetch(s);
@@ -373,17 +401,30 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     const float high_digit = WIDE || g < 4 ? 1.0f : 0x1p-8f, low_digit = WIDE ? 0x1p-8f : high_digit * 0x1p-16f;
     const float start = -12582912.0f * (high_digit + low_digit + (WIDE ? 0x1p-16f : 0.0f));
 
-    float qv[4];
-    if (warp < G) {
-        load_q(qv, a, p, warp, lane);
-        stage_q(qv, a.scale2, sm.q[0][warp], &sm.qscale[0][warp], lane);
-    }
-    __syncthreads();
+    constexpr int kHeads = (kMaxGroup + SPAN - 1) / SPAN;        // heads whose q a warp stages
+    float qv[kHeads][4];
+    auto bring_q = [&](int pair) {
+#pragma unroll
+        for (int i = 0; i < kHeads; i++)
+            if (mate + i * SPAN < G) load_q(qv[i], a, pair, mate + i * SPAN, lane);
+    };
+    auto put_q = [&](int turn) {
+#pragma unroll
+        for (int i = 0; i < kHeads; i++) {
+            const int h = mate + i * SPAN;
+            if (h < G) stage_q(qv[i], a.scale2, sm.q[group][turn][h], &sm.qscale[group][turn][h], lane);
+        }
+    };
+    bring_q(p);
+    put_q(0);
+    sync();
     int turn = 0;
     while (first < end) {                // segments: pairs that have keys
         const int n = quant_len(a.c, p);
         const uint32_t nb = (uint32_t)(n + kQKeys - 1) / kQKeys, stop = min(end, first + nb);
         const bool has = x < stop;
+        if (first >= x0 && mate == 0 && lane == 0)   // this worker has the pair's first block: where its partial results are
+            a.parts[p] = make_uint2(worker, (sm.by_pairs ? (nb + sm.share - 1) / sm.share : (first + nb - 1) / sm.share - worker + 1));
         float2 o[4][4];                  // channels 32r + {0, 16, 8, 24} + g, heads 2t and 2t + 1
         float m = -INFINITY;
         float2 l2 = make_float2(0.0f, 0.0f);
@@ -391,12 +432,12 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         if (has) {
             // a product's rows g and g + 8 hold q's digits 0 and 1, and 2 (WIDE), or g / 4 and g / 4 + 2
             uint32_t qd[4][WIDE ? 6 : 4];
-            const float qscale = head < G ? sm.qscale[turn][head] : 0.0f;
+            const float qscale = head < G ? sm.qscale[group][turn][head] : 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; r++)
 #pragma unroll
                 for (int k = 0; k < (WIDE ? 3 : 2); k++) {
-                    const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[turn][head][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
+                    const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[group][turn][head][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
                     qd[r][k < 2 ? k : 4] = head < G ? d.x : 0u;
                     qd[r][k < 2 ? k + 2 : 5] = head < G ? d.y : 0u;
                 }
@@ -406,7 +447,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
                 for (int h = 0; h < 4; h++) o[r][h] = make_float2(0.0f, 0.0f);
 
 #pragma unroll 1
-            for (; x < stop; x += kQaWarps) {
+            for (; x < stop; x += SPAN) {
                 uint8_t *blk = sm.ring[warp][slot];
                 if (!wait_block(&sm.bar[warp][slot], parity)) late = true;
                 const int b = (int)(x - first), valid = min(kQKeys, n - b * kQKeys);
@@ -536,7 +577,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
                     }
                 }
                 __syncwarp();
-                if (x + kQaWarps < stop) fetch(slot);
+                if (x + SPAN < stop) fetch(slot);
                 else free_slot = slot;   // its block holds the warp's sums until they are merged
                 if (++slot == kQaStages) {
                     slot = 0;
@@ -566,41 +607,45 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         int next = p + 1;                // the next segment's pair, and its q
         if (stop < end) {
             while (block_count(a.c, next) == 0) next++;
-            if (warp < G) load_q(qv, a, next, warp, lane);
+            bring_q(next);
         }
-        __syncthreads();
-        float *part = a.part + (int64_t)(p + blockIdx.x) * G * kQPart;
-        if (warp < G) {                  // head `warp`: lane w has warp w's reference and sum
-            const bool in = lane < kQaWarps && sm.has[lane % kQaWarps] >= 0;
-            const float mw = in ? sm.m[lane][warp] : -INFINITY;
+        sync();
+        float *part = a.part + (int64_t)(p + worker) * G * kQPart;
+#pragma unroll
+        for (int h = mate; h < G; h += SPAN) {       // lane w < SPAN has warp w's reference and sum
+            const int w = group * SPAN + lane % SPAN;
+            const bool in = lane < SPAN && sm.has[w] >= 0;
+            const float mw = in ? sm.m[w][h] : -INFINITY;
             float top = mw;
 #pragma unroll
-            for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+            for (int i = SPAN / 2; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
             const float f = in ? ex2(mw - (top == -INFINITY ? 0.0f : top)) : 0.0f;
-            float l = in ? f * sm.l[lane][warp] : 0.0f;
+            float l = in ? f * sm.l[w][h] : 0.0f;
 #pragma unroll
-            for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(kFull, l, i);
-            if (lane < kQaWarps) sm.factor[lane][warp] = f;
+            for (int i = SPAN / 2; i; i >>= 1) l += __shfl_xor_sync(kFull, l, i);
+            if (lane < SPAN) sm.factor[w][h] = f;
             if (lane == 0) {
-                part[warp * kQPart + kD] = top - kQaLift;
-                part[warp * kQPart + kD + 1] = l;
+                part[h * kQPart + kD] = top - kQaLift;
+                part[h * kQPart + kD + 1] = l;
             }
         }
-        __syncthreads();
-        for (int e = tid; e < G * kD; e += kQaThreads) {
+        sync();
+        for (int e = 32 * mate + lane; e < G * kD; e += 32 * SPAN) {
             const int h = e / kD, c = e % kD;
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kQaWarps; w++)
+            for (int i = 0; i < SPAN; i++) {
+                const int w = group * SPAN + i;
                 if (sm.has[w] >= 0) {
                     const float *so = reinterpret_cast<const float *>(sm.ring[w][sm.has[w]]);
                     sum = fmaf(sm.factor[w][h], WIDE ? so[h * kQaCol + c] : so[h * kQaCol + c] + so[(h + 4) * kQaCol + c], sum);
                 }
+            }
             part[h * kQPart + c] = sum;
         }
         turn ^= 1;
-        if (stop < end && warp < G) stage_q(qv, a.scale2, sm.q[turn][warp], &sm.qscale[turn][warp], lane);
-        __syncthreads();
+        if (stop < end) put_q(turn);
+        sync();
         if (free_slot >= 0) fetch(free_slot);
         first += nb;
         p = next;
@@ -613,7 +658,6 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
 // kernel has ended: it waited for whatever wrote them.
 __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
 {
-    __shared__ uint2 s_sum[kQmThreads / 32], s_plan;
     __shared__ float s_ref[kMaxGroup], s_l[kMaxGroup], s_lse[kMaxGroup];
     const int tid = threadIdx.x, p = blockIdx.y, G = a.G;
     const int n = quant_len(a.c, p);
@@ -621,34 +665,6 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
     const bool is_out = (int)blockIdx.x < outs;
     const int64_t k0 = (int64_t)((int)blockIdx.x - outs) * kQmKeys;
     if (!is_out && k0 >= n) return;
-    // the pair's partial results: slots p + w0 .. p + w0 + ns - 1
-    int w0 = 0, ns = 0;
-    if (n > 0) {
-        if (tid < 32) {
-            uint32_t nb[kQaPer], before = 0, mine = 0;
-            const uint32_t share = plan_pairs(a.c, a.workers, tid, nb);
-            if (share > 0) {
-#pragma unroll
-                for (int i = 0; i < kQaPer; i++) {
-                    const uint32_t k = (nb[i] + share - 1) / share;
-                    if (kQaPer * tid + i < p) before += k;
-                    if (kQaPer * tid + i == p) mine = k;
-                }
-            }
-            before = __reduce_add_sync(kFull, before);
-            mine = __reduce_add_sync(kFull, mine);
-            if (tid == 0) s_plan = make_uint2(before, mine);
-        }
-        __syncthreads();
-        w0 = (int)s_plan.x;
-        ns = (int)s_plan.y;              // 0: not planned by pairs
-        if (ns == 0) {
-            const uint2 blocks = count_blocks<kQmThreads>(a.c, p, s_sum);    // of all pairs, and of those before
-            const uint32_t share = (uint32_t)quant_share(blocks.x, a.workers, kQaMinShare);
-            w0 = (int)(blocks.y / share);
-            ns = (int)((blocks.y + block_count(a.c, p) - 1) / share) - w0 + 1;
-        }
-    }
     pdl_wait();
     if (blockIdx.x == 0 && tid == 0 && quant_len_bad(a.c, p)) quant_devchk(a.c.status, p);
     if (n == 0) {
@@ -656,7 +672,9 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
         if (blockIdx.x == 0 && tid < G && a.lse) a.lse[(int64_t)p * G + tid] = -INFINITY;
         return;
     }
-    const float *part = a.part + (int64_t)(p + w0) * G * kQPart;
+    const uint2 at = a.parts[p];         // the pair's partial results: slots p + at.x .. p + at.x + at.y - 1
+    const int ns = (int)at.y;
+    const float *part = a.part + (int64_t)(p + at.x) * G * kQPart;
     const int warp = tid >> 5, lane = tid & 31;
     const int64_t stride = (int64_t)G * kQPart;
     if (warp < G) {                      // head `warp`: its reference, sum and log-sum
@@ -724,19 +742,25 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
     }
 }
 
-cudaError_t launch_quant_attend(const QuantAttendArgs &a, cudaStream_t s)
+cudaError_t launch_quant_attend(const QuantAttendArgs &args, int num_sms, cudaStream_t s)
 {
-    static std::atomic<int> done[2][kMaxDevices];
-    const int kind = a.G > 4;
-    auto kern = kind ? k_quant_attend<true> : k_quant_attend<false>;
+    static std::atomic<int> done[4][kMaxDevices];
+    QuantAttendArgs a = args;
+    const bool few = a.c.bh >= kQaManyPairs;
+    const int kind = (a.G > 4) + 2 * few;
+    auto kern = kind == 3 ? k_quant_attend<true, kQaFew> : kind == 2 ? k_quant_attend<false, kQaFew>
+              : kind == 1 ? k_quant_attend<true, kQaWarps> : k_quant_attend<false, kQaWarps>;
+    const int ctas = min(num_sms, kQMaxWorkers / kQaGroups);
+    a.span = few ? kQaFew : kQaWarps;
+    a.workers = ctas * (kQaWarps / a.span);
     cudaError_t e = dyn_smem_limit(kern, (int)sizeof(QaSmem), done[kind]);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(a.workers), dim3(kQaThreads), sizeof(QaSmem), s, a);
+    const size_t smem = offsetof(QaSmem, q) + (kQaWarps / a.span) * sizeof(QaSmem::q) / kQaGroups;
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kQaThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     const unsigned parts = a.accumulate ? (unsigned)((a.c.n_cap + kQmKeys - 1) / kQmKeys) : 0u;
     // few pairs have many partial results each: one pass a CTA; many have few: fewer CTAs (256 pairs: 22 us for 24)
-    QuantAttendArgs m = a;
-    m.outs = a.c.bh < a.workers ? (a.G + kQmHeads - 1) / kQmHeads : 1;
-    return launch_pdl(k_quant_merge, dim3(m.outs + parts, a.c.bh), dim3(kQmThreads), 0, s, m);
+    a.outs = a.c.bh < num_sms ? (a.G + kQmHeads - 1) / kQmHeads : 1;
+    return launch_pdl(k_quant_merge, dim3(a.outs + parts, a.c.bh), dim3(kQmThreads), 0, s, a);
 }
 
 }  // namespace pk

@@ -66,6 +66,9 @@ size_t part_bytes(int32_t bh, int32_t G)
     return (n + 255) / 256 * 256;
 }
 
+// bytes of the table of partial results, a multiple of 256
+size_t parts_bytes(int32_t bh) { return ((size_t)bh * sizeof(uint2) + 255) / 256 * 256; }
+
 }  // namespace
 
 extern "C" {
@@ -116,7 +119,7 @@ pk_status pk_quant_attend_workspace(const pk_quant_cache *cache, int32_t group, 
     const pk_status st = check_sizes(cache);
     if (st != PK_OK) return st;
     if (!bytes || group < 1 || group > kMaxGroup) return PK_ERR_INVALID_ARG;
-    *bytes = part_bytes(cache->bh, group);
+    *bytes = part_bytes(cache->bh, group) + parts_bytes(cache->bh);
     if (accumulate) *bytes += (size_t)cache->bh * group * (size_t)cache->n_cap * sizeof(float);
     return PK_OK;
 }
@@ -143,14 +146,14 @@ pk_status pk_quant_attend(const pk_quant_cache *cache, const void *q, int32_t gr
     a.out = out;
     a.lse = lse;
     a.part = (float *)work;
-    a.logits = accumulate ? (float *)((char *)work + part_bytes(cache->bh, group)) : nullptr;
+    a.parts = (uint2 *)((char *)work + part_bytes(cache->bh, group));
+    a.logits = accumulate ? (float *)((char *)a.parts + parts_bytes(cache->bh)) : nullptr;
     a.G = group;
     a.is_bf16 = cache->kv_dtype == PK_BF16;
     a.accumulate = accumulate != 0;
-    a.workers = quant_attend_workers(sms);
     const double s = scale > 0.0f ? (double)scale : 1.0 / std::sqrt((double)kD);
     a.scale2 = (float)(s * 1.4426950408889634074);
-    return quant_status(launch_quant_attend(a, (cudaStream_t)stream));
+    return quant_status(launch_quant_attend(a, sms, (cudaStream_t)stream));
 }
 
 pk_status pk_quant_evict(const pk_quant_cache *src, const pk_quant_cache *dst, int64_t budget, int64_t sink,

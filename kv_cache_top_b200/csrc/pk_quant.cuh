@@ -69,9 +69,10 @@ struct QuantAttendArgs {
     float *out;              // [bh][G][D]
     float *lse;              // [bh][G] or null
     float *part;             // [bh + kQMaxWorkers][G][kQPart]
+    uint2 *parts;            // [bh]: first worker and number of partial results of a pair that has keys
     float *logits;           // [bh][n_cap / 32][G][32] (log2 units) when accumulating, else null
     int32_t G, is_bf16, accumulate;
-    int32_t workers;
+    int32_t workers, span;   // workers, and warps of one
     int32_t outs;            // merge kernel: CTAs per pair that write outputs
     float scale2;            // softmax scale * log2(e)
 };
@@ -82,18 +83,17 @@ struct QuantEvictArgs {
     int32_t *keep;           // [bh][budget] or null
 };
 
-// The blocks of worker w: share = blocks per worker (at least min_share) for
-// `total` blocks; used alike by the attention kernel and its merge.
-__host__ __device__ __forceinline__ int64_t quant_share(int64_t total, int workers, int min_share)
+// Blocks per worker for `total` blocks cut evenly, at least `least`; used alike
+// by the attention kernel and its merge.
+__host__ __device__ __forceinline__ int64_t quant_share(int64_t total, int workers, int least)
 {
     const int64_t s = (total + workers - 1) / workers;
-    return s > min_share ? s : min_share;
+    return s > least ? s : least;
 }
 
 cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s);
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t s);
-cudaError_t launch_quant_attend(const QuantAttendArgs &a, cudaStream_t s);
+cudaError_t launch_quant_attend(const QuantAttendArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s);
-int quant_attend_workers(int num_sms);
 
 }  // namespace pk
