@@ -353,7 +353,8 @@ typedef struct {
  * or a NaN gets the scale NaN: all its values read back as NaN.
  *   k_new, v_new  [bh][src_stride][D] kv_dtype; rows 0..n_new-1 are taken.
  *                 src_stride 0 means n_new.
- *   at            [bh] i32 device, or NULL: lens itself (append at the end).
+ *   at            [bh] i32 device, or NULL: lens itself (append at the end).  It
+ *                 must not overlap lens in part.
  * With acc, the weights of the new slots start at zero.  A pair whose rows do
  * not fit (at < 0 or at + n_new > n_cap) is left as it is, lens included, and
  * the device check records it. */

@@ -212,16 +212,17 @@ __global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a, in
         if (a.c.acc && tid >= j0 && tid < j1) a.c.acc[(int64_t)p * a.c.n_cap + b * kQKeys + tid] = 0.0f;
         if (gridDim.x < tiles) __syncthreads();
     }
-    if (gridDim.x == 1) {                // every thread has read lens: the length may change
+    // the length may change once every CTA of the pair has read it: where one CTA does all, or the places are others'
+    if (gridDim.x == 1 || a.own_at) {
         __syncthreads();
-        if (tid == 0) {
+        if (blockIdx.x == 0 && tid == 0) {
             if (fits) a.c.lens[p] = (int32_t)(at + a.n_rows);
             else quant_devchk(a.c.status, p);
         }
     }
 }
 
-// New lengths after an append of several CTAs per pair.
+// New lengths after an append behind the lengths, of several CTAs per pair.
 __global__ void k_quant_lens(QuantRowsArgs a)
 {
     pdl_wait();
@@ -311,7 +312,7 @@ cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s)
     // up to 4 blocks a pair: one CTA does them in turn and sets the length; a second launch would cost more
     const int tiles = row_tiles(a.n_rows), ctas = tiles <= 4 ? 1 : tiles;
     cudaError_t e = launch_pdl(a.is_bf16 ? k_quant_append<true> : k_quant_append<false>, dim3(ctas, a.c.bh), dim3(kQrThreads), 0, s, a, tiles);
-    if (e == cudaSuccess && ctas > 1)
+    if (e == cudaSuccess && ctas > 1 && !a.own_at)
         e = launch_pdl(k_quant_lens, dim3((a.c.bh + 255) / 256), dim3(256), 0, s, a);
     return e;
 }

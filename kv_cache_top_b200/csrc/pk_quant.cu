@@ -84,11 +84,14 @@ pk_status pk_quant_append(const pk_quant_cache *cache, const void *k_new, const 
     const size_t es = cache->kv_dtype == PK_BF16 ? 2 : 4;
     if (!quant_accessible(k_new, es) || !quant_accessible(v_new, es) || (at && !quant_accessible(at, 4)))
         return PK_ERR_INVALID_ARG;
+    const bool meets = at && overlap(at, (size_t)cache->bh * 4, cache->lens, (size_t)cache->bh * 4);
+    if (meets && at != cache->lens) return PK_ERR_INVALID_ARG;       // one pair's place, another's length
     a.k = k_new;
     a.v = v_new;
     a.n_rows = n_new;
     a.stride = src_stride ? src_stride : n_new;
     a.at = at;
+    a.own_at = at && !meets;
     a.is_bf16 = cache->kv_dtype == PK_BF16;
     a.vec = (uintptr_t)k_new % 16 == 0 && (uintptr_t)v_new % 16 == 0;
     return quant_status(launch_quant_append(a, (cudaStream_t)stream));

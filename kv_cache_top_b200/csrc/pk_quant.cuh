@@ -52,6 +52,7 @@ struct QuantRowsArgs {
     const void *k, *v;       // append: rows in; read back: rows out (cast)
     int64_t n_rows, stride;  // rows taken / rows between pairs
     const int32_t *at;       // first slot per pair, or null
+    int32_t own_at;          // append: `at` does not overlap the lengths
     int32_t is_bf16;
     int32_t vec;             // rows are 16-byte aligned
 };

@@ -245,6 +245,30 @@ def test_append_at_places_and_refuses_what_does_not_fit(pk, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("n_new", [1, 40, 500])
+@pytest.mark.parametrize("where", ["none", "lens"])
+def test_append_places_that_are_the_lengths(pk, n_new, where):
+    """at = None and at = lens itself append at the end; an `at` that overlaps lens in part is refused."""
+    rng = np.random.default_rng(n_new)
+    bh, cap = 3, 1024
+    store = torch.tensor([7, 40, 100, 200], dtype=torch.int32, device="cuda")
+    c, _ = make_cache(pk, rng, [0] * bh, cap, pk.PK_BF16)
+    c = pk.pk_quant_view(c.tensors[0], store[:3], pk.PK_BF16)
+    old = store[:3].tolist()
+    x = make_rows(rng, bh * n_new, torch.bfloat16).view(bh, n_new, D).cuda()
+    with pytest.raises(pk.PkError) as e:
+        pk.pk_quant_append(c, x, x, n_new, at=store[1:])
+    assert e.value.status == pk._lib.PK_ERR_INVALID_ARG
+    pk.pk_quant_append(c, x, x, n_new, at=None if where == "none" else store[:3])
+    got = c.tensors[0].cpu().numpy()
+    assert store[:3].tolist() == [o + n_new for o in old]
+    for p, o in enumerate(old):
+        k, v = ref.values(got[p])
+        val = ref.stored(x[p].float().cpu().numpy())[2]
+        assert np.array_equal(k[o:o + n_new], val) and np.array_equal(v[o:o + n_new], val)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_rows_values_and_untouched_rows(pk, dtype, shift):
