@@ -16,7 +16,7 @@ from ._lib import (KERNELS, PK_BF16, PK_F32, PK_KV_DEVICE, PK_KV_HOST_PINNED, PK
                    PK_QUANT_KEYS, pk_debug_out, pk_info, pk_params, pk_quant_cache)
 
 _handle = None
-_raw_stream = []                         # torch's raw stream getter, once CUDA is initialised
+_current = []                            # torch's getters of the current raw stream and device, once CUDA is initialised
 
 
 def _L():
@@ -59,22 +59,20 @@ def _check(status: int, what: str):
 
 def _ptr(x):
     """Data pointer of a tensor (or an int address, or None)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
+        if _current:                     # torch.cuda.current_stream() makes an object: 3 us a call
+            return _current[0](_current[1]())
         import torch
-        if _raw_stream:                  # torch.cuda.current_stream() makes an object: 3 us a call
-            return _raw_stream[0](torch.cuda.current_device())
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         stream = torch.cuda.current_stream()     # initialises CUDA
-        if raw is not None:
-            _raw_stream.append(raw)
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is not None and device is not None:
+            _current.extend((raw, device))
         return stream.cuda_stream
     if isinstance(stream, int):
         return stream
