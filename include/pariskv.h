@@ -328,7 +328,8 @@ pk_status pk_select_candidates_noalloc(const uint8_t *S, int64_t n, int64_t C, i
  *   status  [2] i32 or NULL: the device-check word of the calls on this cache.
  *           The first failed check writes {PK_ERR_DEVICE_CHECK, pair}; the
  *           caller clears it.  A length outside 0..n_cap is such a check; it
- *           is read as the nearest bound.
+ *           is read as the nearest bound.  (PK_ERR_TIMEOUT in its place: a
+ *           bounded wait for a copy gave up, and results are not valid.)
  * Rows at or behind a pair's length are never read as keys: they may hold any
  * bytes.  The calls leave them as they are.
  * Two calls on one cache must not overlap on the GPU if one of them writes it

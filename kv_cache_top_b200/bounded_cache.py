@@ -93,7 +93,12 @@ class BoundedCache:
         pk_quant_evict(self._cache, dst, self.budget, sink=self.sink, recent=self.recent, keep=self._keep)
         torch.gather(self._pos, 1, self._keep.long(), out=pos[:, :self.budget])
         small = self._cache.n_cap == dst.n_cap            # a longer prompt's buffer is not needed again
-        self._other = (self._cache, self._pos) if small else None
+        if small:
+            self._other = (self._cache, self._pos)
+        else:
+            self._other = None
+            for t in (*self._cache.tensors, self._pos):   # the current stream may not be the one they were made on
+                t.record_stream(torch.cuda.current_stream())
         self._cache, self._pos = dst, pos
         self.n = self.budget
         self.evictions += 1

@@ -338,6 +338,8 @@ def test_attend_lengths_from_none_to_many(pk, dtype, G):
 @pytest.mark.parametrize("dtype,G,lens", [
     ("bf16", 4, [20011]), ("f32", 1, [4096]), ("f32", 8, [9001, 1, 0, 5000]), ("bf16", 8, [8192, 8191]),
     ("bf16", 1, [0]), ("f32", 3, [0, 0, 0]), ("bf16", 4, [577] * 300), ("f32", 2, [1] * 1500 + [40] * 3),
+    ("f32", 5, [0, 700, 33] * 33), ("f32", 8, [90, 0, 31, 700] * 50), ("bf16", 7, [64] * 128), ("bf16", 6, [130] * 129),
+    ("bf16", 3, [33] * 256), ("f32", 8, [65] * 257),
 ])
 def test_attend_splits(pk, dtype, G, lens):
     """Long pairs over many workers, many pairs in one worker, nothing at all."""
@@ -360,6 +362,21 @@ def test_attend_q_off_the_boundary(pk, dtype):
     flat = torch.zeros(2 * 4 * D + 1, dtype=td, device="cuda")
     flat[1:] = make_rows(rng, 8, td).flatten().cuda()
     check_attend(pk, c, blocks, [70, 10], flat[1:].view(2, 4, D), 4)
+
+
+@gpu
+@pytest.mark.parametrize("G", [4, 6])
+def test_attend_weights_off_the_boundary(pk, G):
+    """acc that starts on a 4-byte boundary only."""
+    rng = np.random.default_rng(14)
+    lens = [70, 131, 3]
+    c, blocks = make_cache(pk, rng, lens, 160, pk.PK_BF16)
+    acc0 = rng.random((3, 160)).astype(np.float32)
+    flat = torch.zeros(3 * 160 + 1, device="cuda")
+    flat[1:] = torch.from_numpy(acc0).flatten().cuda()
+    c = pk.pk_quant_view(c.tensors[0], c.tensors[1], pk.PK_BF16, acc=flat[1:].view(3, 160))
+    q = make_rows(rng, 3 * G, torch.bfloat16).view(3, G, D).cuda()
+    check_attend(pk, c, blocks, lens, q, G, accumulate=True, acc0=acc0.astype(np.float64))
 
 
 @gpu
@@ -511,7 +528,63 @@ def test_evict_long_rows(pk):
         check_evict(pk, src, blocks.cpu().numpy(), [n, n - 7], acc, -(-budget // KEYS) * KEYS, pk.PK_F32, budget, 10, 300)
 
 
+@gpu
+@pytest.mark.parametrize("n,cap", [(16384, 16384), (16383, 16384), (16385, 16416), (40000, 40000), (131075, 131104)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_evict_sizes_at_the_borders(pk, n, cap, shift):
+    """Around what a CTA holds at once; acc on 16-byte and on 4-byte boundaries; more pairs than CTAs fit."""
+    bh = 300 if cap < 20000 else 3
+    g = torch.Generator(device="cuda").manual_seed(n)
+    flat = torch.randint(0, 1 << 14, (bh * cap + shift,), generator=g, device="cuda").float()
+    acc = flat[shift:].view(bh, cap)
+    blocks = torch.zeros(bh, cap // KEYS, BLOCK, dtype=torch.uint8, device="cuda")
+    budget, sink, recent = 3000, 5, 100
+    src = pk.pk_quant_view(blocks, torch.full((bh,), n, dtype=torch.int32, device="cuda"), pk.PK_BF16, acc=acc)
+    dst = pk.pk_quant_view(torch.zeros(bh, 94, BLOCK, dtype=torch.uint8, device="cuda"), torch.zeros(bh, dtype=torch.int32, device="cuda"),
+                           pk.PK_BF16, acc=torch.zeros(bh, 94 * KEYS, device="cuda"))
+    keep = torch.zeros(bh, budget, dtype=torch.int32, device="cuda")
+    pk.pk_quant_evict(src, dst, budget, sink=sink, recent=recent, keep=keep)
+    mid = torch.sort(acc[:, sink:n - recent], dim=1, descending=True, stable=True).indices[:, :budget - sink - recent] + sink
+    rest = torch.cat([torch.arange(sink, device="cuda"), torch.arange(n - recent, n, device="cuda")]).expand(bh, -1)
+    want = torch.sort(torch.cat([mid, rest], 1), dim=1).values
+    assert torch.equal(keep.long(), want) and torch.equal(dst.tensors[2][:, :budget], acc.gather(1, want))
+    assert dst.tensors[1].tolist() == [budget] * bh
+
+
 # ---------------------------------------------------------------- together
+@gpu
+def test_first_calls_may_be_captured(pk):
+    """A process whose first calls are recorded into a graph."""
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+    code = """
+import torch, kv_cache_top_b200 as pk
+bh, G = 2, 4
+blocks = torch.zeros(bh, 4, 4608, dtype=torch.uint8, device='cuda')
+c = pk.pk_quant_view(blocks, torch.zeros(bh, dtype=torch.int32, device='cuda'), pk.PK_F32, acc=torch.zeros(bh, 128, device='cuda'))
+e = pk.pk_quant_view(torch.zeros_like(blocks), torch.zeros(bh, dtype=torch.int32, device='cuda'), pk.PK_F32, acc=torch.zeros(bh, 128, device='cuda'))
+x = torch.randn(bh, 5, 128, device='cuda')
+q, out = torch.randn(bh, G, 128, device='cuda'), torch.zeros(bh, G, 128, device='cuda')
+k, v = torch.zeros(bh, 5, 128, device='cuda'), torch.zeros(bh, 5, 128, device='cuda')
+work = torch.empty(pk.pk_quant_attend_workspace(c, G, True), dtype=torch.uint8, device='cuda')
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pk.pk_quant_append(c, x, x, 5)
+    pk.pk_quant_attend(c, q, G, out, work, accumulate=True)
+    pk.pk_quant_evict(c, e, 4)
+    pk.pk_quant_rows(e, 4, k, v)
+g.replay(); g.replay()
+torch.cuda.synchronize()
+assert c.tensors[1].tolist() == [10, 10] and e.tensors[1].tolist() == [4, 4]
+assert abs(float(c.tensors[2].sum()) - 2 * bh * G) < 1e-3 and torch.isfinite(out).all() and float(out.abs().sum()) > 0
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert "captured" in r.stdout, r.stderr[-2000:]
+
+
 @gpu
 def test_calls_in_a_captured_graph_on_another_stream(pk):
     """append + attend + evict recorded once and replayed: the replay sees the lengths and rows of its time."""
