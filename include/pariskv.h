@@ -308,10 +308,11 @@ pk_status pk_select_candidates_noalloc(const uint8_t *S, int64_t n, int64_t C, i
  * rows' bytes, every key attended, and a bounded number of keys.)
  *
  * The cache belongs to the caller: pk_quant_cache only describes its buffers
- * (device memory of the current device); the calls allocate nothing, keep nothing between calls and may be recorded
- * into a CUDA graph.  Each pair bh = b * n_kv_heads + h has its own length
- * lens[bh], read on the GPU by every call, so sequences may be ragged (or
- * empty) and a replayed graph sees the current lengths.
+ * (device memory of the current device); the calls allocate nothing, keep
+ * nothing between calls and may be recorded into a CUDA graph.  Each pair
+ * bh = b * n_kv_heads + h has its own length lens[bh], read on the GPU by every
+ * call, so sequences may be ragged (or empty) and a replayed graph sees the
+ * current lengths.
  *   blocks  [bh][n_cap / 32][4608] bytes, 16-byte aligned.  A block of 32 keys:
  *             [32][64] B  K codes      [32][64] B  V codes
  *             [32][4]     K scales     [32][4]     V scales      (bf16, >= 0)
@@ -398,7 +399,7 @@ pk_status pk_quant_attend(const pk_quant_cache *cache, const void *q, int32_t gr
  *             dst->n_cap >= min(budget, src->n_cap).
  *   budget    >= 1; sink, recent >= 0; sink + recent <= budget.
  *   keep      [bh][budget] i32 or NULL: the kept slots of src, ascending; -1
- *             behind a pair's last. */
+ *             behind a pair's last.  It must not overlap the caches. */
 pk_status pk_quant_evict(const pk_quant_cache *src, const pk_quant_cache *dst, int64_t budget, int64_t sink,
                          int64_t recent, int32_t *keep, void *stream);
 

@@ -4,6 +4,16 @@
 // softmax per worker's segment of a pair and a merge of the segments; when
 // weights are accumulated, the logits go to the workspace and the merge
 // kernel, which knows each head's log-sum, adds the weights to acc.
+//
+// 144 bytes a key of HBM are the floor (64 pairs of 131072 keys, 4 heads: 184
+// us; the kernel takes 268, at a 1770 MHz power cap 300).  What bounds it is
+// the instructions that make matrix operands of codes and sums of digits: 717
+// warp instructions a block of 32 keys, issue slots 65% full, the integer pipe
+// 52%, fp32 44%, matrix 23%.  Hence bytes and not halves for the logits (292
+// us to 275), two fp32 operations an instruction (291 to 276), and 16 warps
+// with two blocks each in flight and not 8 or 12 with more (320 and 296).
+// Calls of few keys are bound by latency: two launches, a plan, one round of
+// blocks and a merge are 9.5 us.
 #include <cuda_fp16.h>
 
 #include "pk_launch.cuh"
@@ -62,22 +72,24 @@ __device__ uint32_t count_blocks(const QuantCache &c, uint32_t *s)
     return v;
 }
 
-// Up to 32 PER pairs, and no more than workers: a worker takes blocks of one
-// pair only, `share` of them, the smallest that does with the workers there
-// are, unless that is more than an even share by over a round of the warps, what
-// a second merge costs (64 ragged pairs of up to 282 blocks: 35 us by pairs, 55
-// evenly; 64 pairs of 4096 blocks, 2 workers for each and 20 idle: 300 and
-// 268).  Else the pairs' blocks are laid end to end and cut
-// evenly.  By one warp: the share, or 0 for even ones; nb[i] is the block count
-// of pair lane + 32 i.
+// nb / share, rounded up; inv = 1 / share
 __device__ __forceinline__ uint32_t ceil_share(uint32_t nb, uint32_t share, float inv)
 {
-    uint32_t q = (uint32_t)((float)nb * inv);        // off by one at most: at most kQMaxWorkers + the pair's round
+    uint32_t q = (uint32_t)((float)nb * inv);        // off by one at most: quotients stay near the number of workers
     int r = (int)(nb - q * share);
     if (r < 0) q--, r += (int)share;
     if (r >= (int)share) q++, r -= (int)share;
     return q + (r > 0);
 }
+
+// Up to 32 PER pairs, and no more than workers: a worker takes blocks of one
+// pair only, `share` of them, the smallest that does with the workers there
+// are, unless that is more than an even share by over a round of the warps,
+// what a second merge costs (64 ragged pairs of up to 282 blocks: 35 us by
+// pairs, 55 evenly; 64 pairs of 4096 blocks, 2 workers for each and 20 idle:
+// 300 and 268).  Else the pairs' blocks are laid end to end and cut evenly.  By
+// one warp: the share, or 0 for even ones; nb[i] is the block count of pair
+// lane + 32 i.
 template <int PER>
 __device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers, int span, int lane, uint32_t nb[PER])
 {

@@ -176,6 +176,11 @@ pk_status pk_quant_evict(const pk_quant_cache *src, const pk_quant_cache *dst, i
     if (overlap(src->blocks, ns, dst->blocks, nd) || overlap(src->lens, (size_t)src->bh * 4, dst->lens, (size_t)dst->bh * 4) ||
         (dst->acc && overlap(src->acc, ws, dst->acc, wd)))
         return PK_ERR_INVALID_ARG;
+    const size_t nk = (size_t)src->bh * (size_t)budget * 4;
+    if (keep && (overlap(keep, nk, src->blocks, ns) || overlap(keep, nk, dst->blocks, nd) || overlap(keep, nk, src->acc, ws) ||
+                 (dst->acc && overlap(keep, nk, dst->acc, wd)) || overlap(keep, nk, src->lens, (size_t)src->bh * 4) ||
+                 overlap(keep, nk, dst->lens, (size_t)dst->bh * 4)))
+        return PK_ERR_INVALID_ARG;       // the kept rows' list, read while the others are written
     a.budget = budget;
     a.sink = sink;
     a.recent = recent;

@@ -147,6 +147,21 @@ def test_gpu_refusals(pk):
     assert c.tensors[1].tolist() == [3, 40] and c.tensors[3].tolist() == [0, 0]
 
 
+@gpu
+def test_evict_list_in_a_cache_is_refused(pk):
+    """keep is read while the caches are written: it lies outside of them."""
+    rng = np.random.default_rng(15)
+    c, _ = make_cache(pk, rng, [40, 64], 64, pk.PK_BF16, acc=np.ones((2, 64)))
+    d, _ = make_cache(pk, rng, [0, 0], 32, pk.PK_BF16, acc=np.zeros((2, 32)))
+    before = [t.clone() for t in (*c.tensors, *d.tensors)]
+    for t in (*c.tensors[:3], *d.tensors[:3]):
+        with pytest.raises(pk.PkError) as e:
+            pk.pk_quant_evict(c, d, 32, keep=t.data_ptr())
+        assert e.value.status == pk._lib.PK_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, t) for x, t in zip(before, (*c.tensors, *d.tensors)))
+
+
 # ---------------------------------------------------------------- rows in and out
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
