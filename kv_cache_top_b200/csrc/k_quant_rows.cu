@@ -74,69 +74,101 @@ __device__ __forceinline__ Raw8 load8(const void *p, int64_t i, int vec)
     return x;
 }
 
-// The word of codes of 8 channels of a group (nibble e: x[e]) and the group's
-// scale bits; the 4 lanes of a group are neighbours.
-template <bool BF16>
-__device__ __forceinline__ uint32_t quant_word(const Raw8 &raw, uint32_t *scale_bits)
+// The codes of a group's 32 channels (x[i].. : channels 8i .. 8i + 7) and its
+// scale bits.  K: word i has channels 8i + e as nibbles e; V: word e / 2 has
+// channels 8i + e as nibbles 4 (e % 2) + i.
+template <bool BF16, bool VALUES>
+__device__ __forceinline__ void quant_group(const Raw8 raw[4], uint32_t word[4], uint32_t *scale_bits)
 {
     // the largest magnitude, as bits: those of infinities and NaN are larger than all others
-    uint32_t top;
-    float x[8];
-    if (BF16) {
-        top = __vmaxu2(__vmaxu2(raw.w[0] & 0x7fff7fffu, raw.w[1] & 0x7fff7fffu),
-                       __vmaxu2(raw.w[2] & 0x7fff7fffu, raw.w[3] & 0x7fff7fffu));
-        top = max(top & 0xffff0000u, top << 16);
+    uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            x[2 * e] = __uint_as_float(raw.w[e] << 16);
-            x[2 * e + 1] = __uint_as_float(raw.w[e] & 0xffff0000u);
-        }
-    } else {
-        top = 0;
+    for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            top = max(top, raw.w[e] & 0x7fffffffu);
-            x[e] = __uint_as_float(raw.w[e]);
-        }
-    }
-    top = max(top, __shfl_xor_sync(kFull, top, 1));
-    top = max(top, __shfl_xor_sync(kFull, top, 2));
+        for (int e = 0; e < (BF16 ? 4 : 8); e++)
+            top = BF16 ? __vmaxu2(top, raw[i].w[e] & 0x7fff7fffu) : max(top, raw[i].w[e] & 0x7fffffffu);
+    if (BF16) top = max(top & 0xffff0000u, top << 16);
     const uint32_t sb = quant_scale_bits(__uint_as_float(top));
     *scale_bits = sb;
     const float s = bf16_bits_f32(sb);
-    if (!(s > 0.0f)) return 0x88888888u;
-    uint32_t word = 0;
-    if (s >= 1e-18f) {
-        // x inv + 1.5 2^23 + 8 rounds to the code in the low bits; codes are joined by adding those bits, shifted, and
-        // taking the constant parts off.  |x| < 7.02 s, so no clamp; a value within rounding of a border is seen by
-        // its remainder, which is exact (see quant_code)
-        float inv;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        constexpr float kMagic = 12582920.0f;
-        uint32_t base = 0;
-        float y[8], far = 0.0f;
+    auto pair = [&](int i, int h) {      // channels 8i + 2h, + 1
+        return BF16 ? make_float2(__uint_as_float(raw[i].w[h] << 16), __uint_as_float(raw[i].w[h] & 0xffff0000u))
+                    : make_float2(__uint_as_float(raw[i].w[2 * h]), __uint_as_float(raw[i].w[2 * h + 1]));
+    };
+    auto place = [&](int i, int e, uint32_t code) {      // or a difference to a code
+        word[VALUES ? e >> 1 : i] += code << (VALUES ? 16 * (e & 1) + 4 * i : 4 * e);
+    };
+    if (!(s > 0.0f)) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            y[e] = fmaf(x[e], inv, kMagic);
-            far = fmaxf(far, fabsf(fmaf(-(y[e] - kMagic), s, x[e])));
-            word += __float_as_uint(y[e]) << (4 * e);
-            base += 0x4b400000u << (4 * e);
+        for (int i = 0; i < 4; i++) word[i] = 0x88888888u;
+        return;
+    }
+    if (s < 1e-18f) {
+        const float up = 18446744073709551616.0f;     // 2^64: 1 / s stays finite
+        const float inv = __fdiv_rn(1.0f, s * up);
+#pragma unroll
+        for (int i = 0; i < 4; i++) word[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int h = 0; h < 4; h++) {
+                const float2 x = pair(i, h);
+                place(i, 2 * h, quant_code(x.x * up, s * up, inv));
+                place(i, 2 * h + 1, quant_code(x.y * up, s * up, inv));
+            }
+        return;
+    }
+    // x inv + 1.5 2^23 + 8 rounds to the code in the low bits; codes are joined by adding those bits, shifted, and
+    // taking the constant parts off.  |x| < 7.02 s, so no clamp
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    constexpr float kMagic = 12582920.0f;
+    uint32_t base = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) base += 0x4b400000u << (4 * e);
+#pragma unroll
+    for (int i = 0; i < 4; i++) word[i] = 0u - base;
+    if (BF16) {
+        // |x / s - (k + 1/2)| = |2 x - (2 k + 1) s| / 2 s is 0 or at least 2^-10: 2 x is a multiple of half a unit of s
+        // from |x| = s / 4 on.  So x inv (off by 2^-19) is rounded to a multiple of 2^-11 first, which makes ties exact
+        // and moves nothing over a border
+        constexpr float kSnap = 6144.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int h = 0; h < 4; h++) {
+                const float2 y = add2(fma2(pair(i, h), make_float2(inv, inv), make_float2(kSnap, kSnap)),
+                                      make_float2(kMagic - kSnap, kMagic - kSnap));
+                place(i, 2 * h, __float_as_uint(y.x));
+                place(i, 2 * h + 1, __float_as_uint(y.y));
+            }
+        return;
+    }
+    // a value within rounding of a border is seen by its remainder, which is exact (see quant_code)
+    auto code = [&](float2 x) { return fma2(x, make_float2(inv, inv), make_float2(kMagic, kMagic)); };
+    auto rest = [&](float2 x, float2 y) { return fma2(add2(y, make_float2(-kMagic, -kMagic)), make_float2(-s, -s), x); };
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int h = 0; h < 4; h++) {
+            const float2 x = pair(i, h), y = code(x), r = rest(x, y);
+            far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+            place(i, 2 * h, __float_as_uint(y.x));
+            place(i, 2 * h + 1, __float_as_uint(y.y));
         }
-        word -= base;
-        if (2.0f * far >= s) {
+    if (2.0f * far < s) return;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float r = fmaf(-(y[e] - kMagic), s, x[e]), d = 2.0f * fabsf(r);
-                if (d > s || (d == s && (__float_as_uint(y[e]) & 1u))) word += (r > 0.0f ? 1u : 0xffffffffu) << (4 * e);
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int h = 0; h < 4; h++) {
+            const float2 x = pair(i, h), y = code(x), r = rest(x, y);
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float re = e ? r.y : r.x, d = 2.0f * fabsf(re);
+                if (d > s || (d == s && (__float_as_uint(e ? y.y : y.x) & 1u))) place(i, 2 * h + e, re > 0.0f ? 1u : 0xffffffffu);
             }
         }
-        return word;
-    }
-    const float up = 18446744073709551616.0f;     // 2^64: 1 / s stays finite
-    const float inv = __fdiv_rn(1.0f, s * up);
-#pragma unroll
-    for (int e = 0; e < 8; e++) word |= quant_code(x[e] * up, s * up, inv) << (4 * e);
-    return word;
 }
 
 // Transpose of the 4 x 4 bytes of 4 neighbouring lanes' words: lane i gets
@@ -149,59 +181,48 @@ __device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane)
     return (lane & 2) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
 }
 
-// nibbles 0, 2, 4, 6 of a word of bytes 0x0n, and back
-__device__ __forceinline__ uint32_t join_nibbles(uint32_t x)
-{
-    x = (x | x >> 4) & 0x00ff00ffu;
-    return (x | x >> 8) & 0xffffu;
-}
+// nibbles 0..3 as the bytes 0x0n of a word
 __device__ __forceinline__ uint32_t spread_nibbles(uint32_t x)
 {
     x = (x | x << 8) & 0x00ff00ffu;
     return (x | x << 4) & 0x0f0f0f0fu;
 }
 
-// One CTA per 32-key block of the cache (or, of few rows, per pair).  A warp
-// has rows 4w .. 4w + 3, two at a time: lane (row, group r, quarter t) has
-// channels 32r + 8t .. + 7, whose codes are word (t, r) of a K row; of a V row
-// they are nibble t of the 8 chunks, which the 4 lanes of a group exchange.
+// One CTA per 32-key block of the cache (or, of few rows, per pair).  A thread
+// has a group of 32 channels of a row of K or V: what a group needs once (the
+// scale) is then computed once, and codes are put in place without a shuffle.
 // The block is put together in shared memory and leaves by 16-byte stores.
 template <bool BF16>
 __global__ void __launch_bounds__(kQrThreads) k_quant_append(QuantRowsArgs a, int tiles)
 {
     __shared__ __align__(16) uint8_t img[kQBlock];
-    const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int p = blockIdx.y, tid = threadIdx.x;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : a.c.lens[p];
     const bool fits = at >= 0 && at + a.n_rows <= a.c.n_cap;
-    const int r = (lane & 15) >> 2, t = lane & 3;
+    const int j = tid >> 2 & 31, r = tid & 3;
     for (int tile = blockIdx.x; fits && tile < tiles; tile += gridDim.x) {
         const int64_t b = at / kQKeys + tile, i0 = b * kQKeys - at;          // row of the block's first key
         if (i0 >= a.n_rows) break;
         const int j0 = (int)max((int64_t)0, -i0), j1 = (int)min((int64_t)kQKeys, a.n_rows - i0);
-        if (4 * warp < j1 && 4 * warp + 4 > j0) {
-            const int64_t base = ((int64_t)p * a.stride + i0) * kD + 8 * (lane & 15);
-            Raw8 x[4];                   // K rows 4w + 2i + lane / 16, then V
+        if (j >= j0 && j < j1) {
+            const int64_t base = ((int64_t)p * a.stride + i0 + j) * kD + 32 * r;
+            const bool values = tid >= 4 * kQKeys;
+            Raw8 x[4];
+            uint32_t w[4], sb;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = 4 * warp + 2 * (i & 1) + (lane >> 4);
-                x[i] = Raw8{};
-                if (j >= j0 && j < j1) x[i] = load8<BF16>(i >> 1 ? a.v : a.k, base + (int64_t)j * kD, a.vec);
-            }
+            for (int i = 0; i < 4; i++) x[i] = load8<BF16>(values ? a.v : a.k, base + 8 * i, a.vec);
+            if (values) {
+                quant_group<BF16, true>(x, w, &sb);
+                uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = 4 * warp + 2 * (i & 1) + (lane >> 4);
-                uint32_t sb, w = quant_word<BF16>(x[i], &sb);
-                if (i >> 1) {
-                    w = transpose_bytes(w, lane);      // byte i: channels 8i + 2t, + 1 of the group
-                    uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
-                    *reinterpret_cast<uint16_t *>(row + 8 * ((2 * t) ^ v_turn(j))) = (uint16_t)join_nibbles(w & 0x0f0f0f0fu);
-                    *reinterpret_cast<uint16_t *>(row + 8 * ((2 * t + 1) ^ v_turn(j))) = (uint16_t)join_nibbles(w >> 4 & 0x0f0f0f0fu);
-                } else {
-                    *reinterpret_cast<uint32_t *>(img + j * kQRow + 16 * t + 4 * r) = w;
-                }
-                if (t == 0) *reinterpret_cast<uint16_t *>(img + (i >> 1 ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
+                for (int g = 0; g < 8; g++) *reinterpret_cast<uint16_t *>(row + 8 * (g ^ v_turn(j))) = (uint16_t)(w[g >> 1] >> (16 * (g & 1)));
+            } else {
+                quant_group<BF16, false>(x, w, &sb);
+#pragma unroll
+                for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t *>(img + j * kQRow + 16 * i + 4 * r) = w[i];
             }
+            *reinterpret_cast<uint16_t *>(img + (values ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
         }
         __syncthreads();
         uint8_t *dst = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
