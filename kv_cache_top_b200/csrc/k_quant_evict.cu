@@ -12,12 +12,16 @@
 // rows: reading acc again costs less than cluster barriers (64 pairs of 1600
 // keys: 24 us for 29).
 // k_quant_select, k_quant_gather, longer pairs: a cluster selects, each CTA a
-// run of slots that it reads for every digit (from L2 after the first time);
-// histograms are joined through distributed shared memory, and a CTA's own
-// counts above the threshold give its places.  The list of kept slots goes to
-// `keep`, or to dst's acc (whose weights the gather writes in their place), and
-// a second kernel moves the rows, all SMs' memory pipes full.  With neither,
-// the cluster moves them itself.
+// run of slots; histograms are joined through distributed shared memory, and a
+// CTA's own counts above the threshold give its places.  A run is read twice
+// (from L2 the second time): for the first digit, and to mark the slots above
+// it and put aside those that agree with it, which alone the other digits need
+// (64 pairs of 131072 keys to 4096: 43 us, 55 with a pass for each digit and
+// one for the marks).  Runs that are too long, or have too many that agree, do
+// take those passes.  The list of kept slots goes to `keep`, or to dst's acc
+// (whose weights the gather writes in their place), and a second kernel moves
+// the rows, all SMs' memory pipes full.  With neither, the cluster moves them
+// itself.
 #include <cooperative_groups.h>
 
 #include "pk_launch.cuh"
@@ -46,14 +50,19 @@ struct QeSmem {
 static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots");
 
 constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (66 us for 50)
+constexpr int kQsMarked = 32768;         // slots of a run that are marked in the second pass
+constexpr int kQsCands = 3584;           // of them, that agree with the first digit of the threshold
 struct QsSmem {
-    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts
+    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts; later the marks, and the keys of the slots below or a list
     uint32_t sums[kQeBins];              // all CTAs' counts
     uint32_t ws[kQsThreads / 32 + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
+    uint32_t cands;
+    uint16_t cand[kQsCands];             // slots whose first digit is the threshold's, in any order
 };
-static_assert(kQsChunk * 2 <= 2 * kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4, "a chunk's list and marks take the place of the copies");
+static_assert(kQsMarked / 4 <= kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4 && kQsChunk * 2 <= 2 * kQeBins * 4 && kQsCands <= 2 * kQeBins,
+              "marks, keys and a chunk's list take the place of the copies");
 
 // digit d of the select: its place, its bins, and the bits above it
 struct Digit {
@@ -314,6 +323,31 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         }
     };
 
+    // f(weights, i) for the slots i .. i + 3 of [from, stop), 4 loads in flight
+    auto each = [&](int from, int stop, auto &&f) {
+        int i = from + 4 * tid;
+        for (; vec && i + 12 * kQsThreads + 4 <= stop; i += 16 * kQsThreads) {
+            float4 v[4];
+#pragma unroll
+            for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
+#pragma unroll
+            for (int h = 0; h < 4; h++) {
+                const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                f(x, i + 4 * h * kQsThreads);
+            }
+        }
+        for (; i < stop; i += 4 * kQsThreads) {
+            float x[4];
+            weights(x, i);
+            f(x, i);
+        }
+    };
+
+    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[1]);
+    uint32_t *cand_key = sm.hist[2];
+    const bool once = c1 - c0 <= kQsMarked;
+    bool marks_done = false;
+    if (tid == 0) sm.cands = 0;
     // threshold key, and how many of the keys equal to it stay; own: this CTA's contested keys above it
     uint32_t prefix = 0, left = q.need, own = 0, ties = 0;
     if (q.need) {
@@ -343,21 +377,32 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                     if (i + e >= first && i + e < end && (k & g.above) == prefix) atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
                 }
             };
-            int i = first / 4 * 4 + 4 * tid;
-            for (; vec && i + 12 * kQsThreads + 4 <= c1 && i < end; i += 16 * kQsThreads) {      // 4 loads in flight
-                float4 v[4];
+            // second digit: also marks the slots above the first, and lists those that agree with it
+            auto count_and_mark = [&](const float x[4], int i) {
+                uint32_t keep = 0;
 #pragma unroll
-                for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
-#pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-                    count(x, i + 4 * h * kQsThreads);
+                for (int e = 0; e < 4; e++) {
+                    const bool in = i + e >= first && i + e < end;
+                    const bool above = nan ? x[e] == x[e] : x[e] > high;
+                    keep |= (uint32_t)(!in || above) << e;
+                    if (in && (nan ? x[e] != x[e] : x[e] >= low && x[e] <= high)) {
+                        const uint32_t k = weight_key(x[e]), at = atomicAdd(&sm.cands, 1u);
+                        atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
+                        if (at < kQsCands) {
+                            cand_key[at] = k;
+                            sm.cand[at] = (uint16_t)(i + e - c0);
+                        }
+                    }
                 }
-            }
-            for (; i < end; i += 4 * kQsThreads) {
-                float x[4];
-                weights(x, i);
-                count(x, i);
+                marks[(i - c0) >> 2] = (uint8_t)keep;
+            };
+            if (d == 1 && once) {
+                each(c0, c1, count_and_mark);
+            } else if (marks_done) {
+                for (int i = tid; i < (int)sm.cands; i += kQsThreads)
+                    if ((cand_key[i] & g.above) == prefix) atomicAdd(&hist[(cand_key[i] >> g.shift) & (g.bins - 1)], 1u);
+            } else {
+                each(first / 4 * 4, end, count);
             }
             if (d == 0) {
                 __syncthreads();
@@ -389,8 +434,14 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             for (int i = tid; i < g.bins; i += kQsThreads)
                 if (i > (int)digit) own += sm.hist[0][i];
             if (d == 2) ties = sm.hist[0][digit];
+            if (d == 1) marks_done = once && sm.cands <= kQsCands;
             __syncthreads();
         }
+        if (marks_done)                  // the other slots that stay or tie
+            for (int i = tid; i < (int)sm.cands; i += kQsThreads) {
+                const uint32_t k = cand_key[i], j = sm.cand[i];
+                if (k >= prefix) atomicOr(&sm.hist[1][j >> 4], 1u << (8 * (j >> 2 & 3) + (j & 3) + (k == prefix ? 4 : 0)));
+            }
     }
     // kept slots before this CTA's
     uint32_t before = 0, ties_before = 0;
@@ -412,8 +463,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         cluster.barrier_arrive();                    // the other CTAs' memory has been read
     }
     int *list = kept_list(a, p);
-    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.hist[0]);
-    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[2]);
+    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.hist[2]);
     const bool nan = prefix == 0;                    // the threshold is NaN: all others are above it
     const float limit = nan ? 0.0f : key_weight(prefix);
     for (int c = c0; c < c1; c += kQsChunk) {
@@ -429,26 +479,11 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             marks[(i - c) >> 2] = (uint8_t)(keep | tie << 4);
         };
         const int stop = min(c1, c + kQsChunk);
-        int i = c + 4 * tid;
-        for (; vec && i + 12 * kQsThreads + 4 <= stop; i += 16 * kQsThreads) {       // 4 loads in flight
-            float4 v[4];
-#pragma unroll
-            for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
-#pragma unroll
-            for (int h = 0; h < 4; h++) {
-                const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-                mark(x, i + 4 * h * kQsThreads);
-            }
-        }
-        for (; i < stop; i += 4 * kQsThreads) {
-            float x[4];
-            weights(x, i);
-            mark(x, i);
-        }
+        if (!marks_done) each(c, stop, mark);
         __syncthreads();
         uint32_t keep, tie, total;
         const int i0 = c + 32 * tid;
-        marked(marks + 8 * tid, stop - i0, &keep, &tie);
+        marked(marks + (marks_done ? (c - c0) / 4 : 0) + 8 * tid, stop - i0, &keep, &tie);
         const uint32_t scan = block_excl_scan<kQsThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
         uint32_t rest = ties_before + (scan & 0xffffu), at = (scan >> 16) + min(rest, left) - min(ties_before, left);
         const int kept = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));

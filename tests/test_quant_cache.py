@@ -566,6 +566,43 @@ def test_evict_sizes_at_the_borders(pk, n, cap, shift):
     assert dst.tensors[1].tolist() == [budget] * bh
 
 
+@gpu
+@pytest.mark.parametrize("n", [131104, 270000, 40000])
+@pytest.mark.parametrize("kind", ["equal", "few", "part", "near", "nan", "inf"])
+def test_evict_crowded_weights(pk, n, kind):
+    """Weights that agree in their first bits: everywhere, in a part of the slots, or in all but the last bits."""
+    bh, budget, sink, recent = 2, 2500, 7, 33
+    cap = -(-n // KEYS) * KEYS
+    g = torch.Generator(device="cuda").manual_seed(n)
+    acc = torch.rand(bh, cap, generator=g, device="cuda")
+    if kind == "equal":
+        acc[:] = 0.25
+    elif kind == "few":
+        acc = torch.randint(0, 3, (bh, cap), generator=g, device="cuda").float()
+    elif kind == "part":                 # the threshold falls on a value that fills one stretch
+        acc *= 0.5
+        acc[:, n // 3:n // 3 + 6000] = 0.75
+        acc[:, 100:300] = 0.9
+    elif kind == "near":
+        acc = (0x3f800000 + torch.randint(0, 1 << 12, (bh, cap), generator=g, device="cuda", dtype=torch.int32)).view(torch.float32)
+    elif kind == "nan":                  # the threshold is NaN: fewer others than the budget
+        acc[:, 1000:] = float("nan")
+    elif kind == "inf":
+        acc[:, 500:9000] = float("inf")
+    src = pk.pk_quant_view(torch.zeros(bh, cap // KEYS, BLOCK, dtype=torch.uint8, device="cuda"),
+                           torch.full((bh,), n, dtype=torch.int32, device="cuda"), pk.PK_F32, acc=acc)
+    dst = pk.pk_quant_view(torch.zeros(bh, 79, BLOCK, dtype=torch.uint8, device="cuda"), torch.zeros(bh, dtype=torch.int32, device="cuda"),
+                           pk.PK_F32, acc=torch.zeros(bh, 79 * KEYS, device="cuda"))
+    keep = torch.zeros(bh, budget, dtype=torch.int32, device="cuda")
+    pk.pk_quant_evict(src, dst, budget, sink=sink, recent=recent, keep=keep)
+    order = torch.where(acc.isnan(), float("-inf"), acc)[:, sink:n - recent]
+    mid = torch.sort(order, dim=1, descending=True, stable=True).indices[:, :budget - sink - recent] + sink
+    rest = torch.cat([torch.arange(sink, device="cuda"), torch.arange(n - recent, n, device="cuda")]).expand(bh, -1)
+    want = torch.sort(torch.cat([mid, rest], 1), dim=1).values
+    assert torch.equal(keep.long(), want)
+    assert torch.equal(dst.tensors[2][:, :budget].view(torch.int32), acc.gather(1, want).view(torch.int32))
+
+
 # ---------------------------------------------------------------- together
 @gpu
 def test_first_calls_may_be_captured(pk):
