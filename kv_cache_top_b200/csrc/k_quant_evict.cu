@@ -16,7 +16,7 @@
 // CTA's own counts above the threshold give its places.  A run is read twice
 // (from L2 the second time): for the first digit, and to mark the slots above
 // it and put aside those that agree with it, which alone the other digits need
-// (64 pairs of 131072 keys to 4096: 43 us, 55 with a pass for each digit and
+// (64 pairs of 131072 keys to 4096: 38 us, 55 with a pass for each digit and
 // one for the marks).  Runs that are too long, or have too many that agree, do
 // take those passes.  The list of kept slots goes to `keep`, or to dst's acc
 // (whose weights the gather writes in their place), and a second kernel moves
@@ -377,26 +377,42 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                     if (i + e >= first && i + e < end && (k & g.above) == prefix) atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
                 }
             };
-            // second digit: also marks the slots above the first, and lists those that agree with it
+            // first digit: of all contested slots
+            auto count_first = [&](const float x[4], int i) {
+                if (i >= first && i + 4 <= end) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) atomicAdd(&hist[weight_key(x[e]) >> 21], 1u);
+                } else {
+                    count(x, i);
+                }
+            };
+            // second digit: also marks the slots above the first, and puts aside those that agree with it
             auto count_and_mark = [&](const float x[4], int i) {
-                uint32_t keep = 0;
+                uint32_t above = 0, from = 0, in = 15;
+                if (i < first || i + 4 > end) {
+                    in = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) in |= (uint32_t)(i + e >= first && i + e < end) << e;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const bool in = i + e >= first && i + e < end;
-                    const bool above = nan ? x[e] == x[e] : x[e] > high;
-                    keep |= (uint32_t)(!in || above) << e;
-                    if (in && (nan ? x[e] != x[e] : x[e] >= low && x[e] <= high)) {
-                        const uint32_t k = weight_key(x[e]), at = atomicAdd(&sm.cands, 1u);
-                        atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
-                        if (at < kQsCands) {
-                            cand_key[at] = k;
-                            sm.cand[at] = (uint16_t)(i + e - c0);
-                        }
+                    above |= (uint32_t)(nan ? x[e] == x[e] : x[e] > high) << e;
+                    from |= (uint32_t)(nan || x[e] >= low) << e;
+                }
+                marks[(i - c0) >> 2] = (uint8_t)((above | ~in) & 15u);
+                for (uint32_t c = from & ~above & in; c; c &= c - 1) {
+                    const int e = __ffs(c) - 1;
+                    const uint32_t k = weight_key(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3]), at = atomicAdd(&sm.cands, 1u);
+                    atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
+                    if (at < kQsCands) {
+                        cand_key[at] = k;
+                        sm.cand[at] = (uint16_t)(i + e - c0);
                     }
                 }
-                marks[(i - c0) >> 2] = (uint8_t)keep;
             };
-            if (d == 1 && once) {
+            if (d == 0) {
+                each(first / 4 * 4, end, count_first);
+            } else if (d == 1 && once) {
                 each(c0, c1, count_and_mark);
             } else if (marks_done) {
                 for (int i = tid; i < (int)sm.cands; i += kQsThreads)
