@@ -51,18 +51,21 @@ static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots")
 
 constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (66 us for 50)
 constexpr int kQsMarked = 32768;         // slots of a run that are marked in the second pass
-constexpr int kQsCands = 3584;           // of them, that agree with the first digit of the threshold
+constexpr int kQsCands = 3584;           // of them, put aside: they agree with the first digit of the threshold
+constexpr int kQsShared = 8192;          // put aside by all CTAs, up to which each takes all of them itself
 struct QsSmem {
-    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts; later the marks, and the keys of the slots below or a list
-    uint32_t sums[kQeBins];              // all CTAs' counts
+    uint32_t sums[kQeBins];              // all CTAs' counts; at the end, with hist[0], a chunk's list
+    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts; 1, 2: later the keys of `cand`, 3: marks
     uint32_t ws[kQsThreads / 32 + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
+    uint32_t all[kQeMaxCluster];         // `cands` of the cluster's CTAs
+    uint32_t ahead[2];                   // of the CTAs before: slots put aside that stay, and that tie
     uint32_t cands;
     uint16_t cand[kQsCands];             // slots whose first digit is the threshold's, in any order
 };
-static_assert(kQsMarked / 4 <= kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4 && kQsChunk * 2 <= 2 * kQeBins * 4 && kQsCands <= 2 * kQeBins,
-              "marks, keys and a chunk's list take the place of the copies");
+static_assert(kQsMarked / 4 <= kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4 && kQsCands <= 2 * kQeBins, "marks and keys take the place of the copies");
+static_assert(offsetof(QsSmem, hist) == sizeof(QsSmem::sums) && kQsChunk * 2 <= 2 * kQeBins * 4, "a chunk's list is in sums and hist[0]");
 
 // digit d of the select: its place, its bins, and the bits above it
 struct Digit {
@@ -343,11 +346,28 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         }
     };
 
-    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[1]);
-    uint32_t *cand_key = sm.hist[2];
-    const bool once = c1 - c0 <= kQsMarked;
-    bool marks_done = false;
-    if (tid == 0) sm.cands = 0;
+    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[3]);
+    uint32_t *cand_key = sm.hist[1];
+    const bool once = run <= kQsMarked;
+    bool marks_done = false, alone = false;
+    const uint32_t others = (uint32_t)(c1 - c0 - max(0, min(c1, q.hi) - max(c0, q.lo)));       // not contested
+    if (tid == 0) {
+        sm.cands = sm.ahead[0] = sm.ahead[1] = 0;
+        sm.count[0] = others;
+    }
+    // f(key) for the keys that the first `upto` CTAs have put aside
+    auto each_cand = [&](int upto, auto &&f) {
+        uint32_t most = 0;
+        for (int w = 0; w < upto; w++) most = max(most, sm.all[w]);
+        for (uint32_t i = tid; i < most; i += kQsThreads) {
+            uint32_t k[kQeMaxCluster];
+#pragma unroll
+            for (int w = 0; w < kQeMaxCluster; w++) k[w] = w < upto && i < sm.all[w] ? cluster.map_shared_rank(cand_key, w)[i] : 0u;
+#pragma unroll
+            for (int w = 0; w < kQeMaxCluster; w++)
+                if (w < upto && i < sm.all[w]) f(k[w]);
+        }
+    };
     // threshold key, and how many of the keys equal to it stay; own: this CTA's contested keys above it
     uint32_t prefix = 0, left = q.need, own = 0, ties = 0;
     if (q.need) {
@@ -429,7 +449,36 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                     sm.hist[0][i] = v;
                 }
             }
+            if (d == 1 && once) {
+                const uint32_t above = __reduce_add_sync(kFull, own);
+                if (lane == 0) atomicAdd(&sm.count[0], above);
+            }
             cluster.sync();
+            if (d == 1 && once) {
+                if (tid < ranks) sm.all[tid] = *cluster.map_shared_rank(&sm.cands, tid);
+                __syncthreads();
+                uint32_t total = 0, most = 0;
+                for (int w = 0; w < ranks; w++) total += sm.all[w], most = max(most, sm.all[w]);
+                alone = most <= kQsCands && total <= kQsShared;
+            }
+            if (alone) {                 // the other digits without the other CTAs' help
+                marks_done = true;
+#pragma unroll 1
+                for (int e = 1; e < 3; e++) {
+                    const Digit h = digit_of(e);
+                    for (int i = tid; i < h.bins; i += kQsThreads) sm.sums[i] = 0;
+                    __syncthreads();
+                    each_cand(ranks, [&](uint32_t k) {
+                        if ((k & h.above) == prefix) atomicAdd(&sm.sums[(k >> h.shift) & (h.bins - 1)], 1u);
+                    });
+                    __syncthreads();
+                    find_digit<kQsThreads>(sm.sums, h.bins, sm.ws, left, &sm.digit, &sm.left);
+                    prefix |= sm.digit << h.shift;
+                    left = sm.left;
+                    __syncthreads();
+                }
+                break;
+            }
             // each CTA joins the counts of its share of the bins and gives all the sums
             const int share = g.bins / ranks;
             for (int i = tid; i < share; i += kQsThreads) {
@@ -456,15 +505,30 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         if (marks_done)                  // the other slots that stay or tie
             for (int i = tid; i < (int)sm.cands; i += kQsThreads) {
                 const uint32_t k = cand_key[i], j = sm.cand[i];
-                if (k >= prefix) atomicOr(&sm.hist[1][j >> 4], 1u << (8 * (j >> 2 & 3) + (j & 3) + (k == prefix ? 4 : 0)));
+                if (k >= prefix) atomicOr(&sm.hist[3][j >> 4], 1u << (8 * (j >> 2 & 3) + (j & 3) + (k == prefix ? 4 : 0)));
             }
     }
     // kept slots before this CTA's
     uint32_t before = 0, ties_before = 0;
-    {
+    if (alone) {
+        uint32_t above = 0, equal = 0;
+        each_cand(rank, [&](uint32_t k) { above += k > prefix, equal += k == prefix; });
+        above = __reduce_add_sync(kFull, above);
+        equal = __reduce_add_sync(kFull, equal);
+        if (lane == 0) {
+            atomicAdd(&sm.ahead[0], above);
+            atomicAdd(&sm.ahead[1], equal);
+        }
+        for (int w = 0; w < rank; w++) before += *cluster.map_shared_rank(sm.count, w);
+        __syncthreads();
+        before += sm.ahead[0];
+        ties_before = sm.ahead[1];
+        before += min(ties_before, left);            // ties that stay are the lowest
+        cluster.barrier_arrive();                    // the other CTAs' memory has been read
+    } else {
         own = __reduce_add_sync(kFull, own);
         if (tid == 0) {
-            sm.count[0] = (uint32_t)(c1 - c0 - max(0, min(c1, q.hi) - max(c0, q.lo)));       // not contested
+            sm.count[0] = others;
             sm.count[1] = ties;
         }
         __syncthreads();
@@ -475,11 +539,11 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             before += o[0];
             ties_before += o[1];
         }
-        before += min(ties_before, left);            // ties that stay are the lowest
-        cluster.barrier_arrive();                    // the other CTAs' memory has been read
+        before += min(ties_before, left);
+        cluster.barrier_arrive();
     }
     int *list = kept_list(a, p);
-    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.hist[2]);
+    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.sums);     // which other CTAs no longer read (nor hist[0])
     const bool nan = prefix == 0;                    // the threshold is NaN: all others are above it
     const float limit = nan ? 0.0f : key_weight(prefix);
     for (int c = c0; c < c1; c += kQsChunk) {
