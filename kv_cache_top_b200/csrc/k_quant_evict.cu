@@ -34,8 +34,7 @@ namespace pk {
 constexpr int kQeThreads = 512;
 constexpr int kQeBins = 2048;
 constexpr int kQeTile = 16384;           // slots in shared memory: two CTAs to an SM
-constexpr int kQsThreads = 256;          // select
-constexpr int kQsChunk = 32 * kQsThreads;     // slots listed at once, 32 consecutive ones a thread
+constexpr int kQgThreads = 256;          // gather
 constexpr int kQeMaxCluster = 8;
 
 struct QeSmem {
@@ -49,23 +48,48 @@ struct QeSmem {
 };
 static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots");
 
+// The select's CTAs: of 256 threads, 4 to an SM, where there are many pairs; of
+// 1024 where each has an SM for itself: four times the loads in flight, and
+// room for the marks of a longer run (4 pairs of 1048576 keys: 56 us
+// for 122).
 constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (66 us for 50)
-constexpr int kQsMarked = 32768;         // slots of a run that are marked in the second pass
-constexpr int kQsCands = 3584;           // of them, put aside: they agree with the first digit of the threshold
-constexpr int kQsShared = 8192;          // put aside by all CTAs, up to which each takes all of them itself
-struct QsSmem {
-    uint32_t sums[kQeBins];              // all CTAs' counts; at the end, with hist[0], a chunk's list
-    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts; 1, 2: later the keys of `cand`, 3: marks
-    uint32_t ws[kQsThreads / 32 + 1];
+constexpr int kQsMany = 256, kQsFew = 1024;
+template <int NT>
+struct QsState {
+    uint32_t ws[NT / 32 + 1];
     uint32_t digit, left;
     uint32_t count[2];                   // kept and tied slots of this CTA
     uint32_t all[kQeMaxCluster];         // `cands` of the cluster's CTAs
     uint32_t ahead[2];                   // of the CTAs before: slots put aside that stay, and that tie
-    uint32_t cands;
-    uint16_t cand[kQsCands];             // slots whose first digit is the threshold's, in any order
+    uint32_t cands;                      // slots put aside, in any order: they agree with the threshold in the first digit
 };
-static_assert(kQsMarked / 4 <= kQeBins * 4 && kQsChunk / 4 <= kQeBins * 4 && kQsCands <= 2 * kQeBins, "marks and keys take the place of the copies");
-static_assert(offsetof(QsSmem, hist) == sizeof(QsSmem::sums) && kQsChunk * 2 <= 2 * kQeBins * 4, "a chunk's list is in sums and hist[0]");
+template <int NT>
+struct QsSmem : QsState<NT> {
+    static constexpr int kMarked = 262144, kCands = 6144;        // slots of a run that are marked in the second pass; put aside
+    uint32_t sums[kQeBins];              // all CTAs' counts
+    uint32_t hist[kQsCopies][kQeBins];   // this CTA's counts
+    uint32_t key[kCands];                // of the slots put aside
+    uint32_t cand[kCands];
+    alignas(16) uint8_t mark[kMarked / 4];
+    uint16_t list[32 * NT];              // kept slots of 32 a thread
+    __device__ uint32_t *keys() { return key; }
+    __device__ uint8_t *marks() { return mark; }
+    __device__ uint16_t *chunk() { return list; }
+};
+template <>
+struct QsSmem<kQsMany> : QsState<kQsMany> {
+    static constexpr int kMarked = 32768, kCands = 3584;
+    alignas(16) uint32_t sums[kQeBins];  // at the end, with hist[0], the list: other CTAs no longer read them
+    uint32_t hist[kQsCopies][kQeBins];   // 1, 2: later the keys, 3: marks
+    uint16_t cand[kCands];
+    __device__ uint32_t *keys() { return hist[1]; }
+    __device__ uint8_t *marks() { return reinterpret_cast<uint8_t *>(hist[3]); }
+    __device__ uint16_t *chunk() { return reinterpret_cast<uint16_t *>(sums); }
+};
+static_assert(QsSmem<kQsMany>::kMarked / 4 <= kQeBins * 4 && 8 * kQsMany <= kQeBins * 4 && QsSmem<kQsMany>::kCands <= 2 * kQeBins &&
+              2 * 32 * kQsMany <= 2 * kQeBins * 4, "marks, keys and the list fit where they are put");
+static_assert(sizeof(QsSmem<kQsMany>) <= 48 * 1024 && sizeof(QsSmem<kQsFew>) <= 227 * 1024, "4 CTAs to an SM, and one");
+constexpr int kQsShared = 8192;          // put aside by all CTAs, up to which each takes all of them itself
 
 // digit d of the select: its place, its bins, and the bits above it
 struct Digit {
@@ -303,9 +327,10 @@ __device__ __forceinline__ int *kept_list(const QuantEvictArgs &a, int p)
     return a.keep ? a.keep + p * a.budget : a.dst.acc ? reinterpret_cast<int *>(a.dst.acc + p * a.dst.n_cap) : nullptr;
 }
 
-__global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a)
+template <int NT>
+__device__ __forceinline__ void quant_select(const QuantEvictArgs &a, QsSmem<NT> &sm)
 {
-    __shared__ QsSmem sm;
+    using Smem = QsSmem<NT>;
     cg::cluster_group cluster = cg::this_cluster();
     const int p = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -329,26 +354,26 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
     // f(weights, i) for the slots i .. i + 3 of [from, stop), 4 loads in flight
     auto each = [&](int from, int stop, auto &&f) {
         int i = from + 4 * tid;
-        for (; vec && i + 12 * kQsThreads + 4 <= stop; i += 16 * kQsThreads) {
+        for (; vec && i + 12 * NT + 4 <= stop; i += 16 * NT) {
             float4 v[4];
 #pragma unroll
-            for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * kQsThreads);
+            for (int h = 0; h < 4; h++) v[h] = *reinterpret_cast<const float4 *>(acc + i + 4 * h * NT);
 #pragma unroll
             for (int h = 0; h < 4; h++) {
                 const float x[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-                f(x, i + 4 * h * kQsThreads);
+                f(x, i + 4 * h * NT);
             }
         }
-        for (; i < stop; i += 4 * kQsThreads) {
+        for (; i < stop; i += 4 * NT) {
             float x[4];
             weights(x, i);
             f(x, i);
         }
     };
 
-    uint8_t *marks = reinterpret_cast<uint8_t *>(sm.hist[3]);
-    uint32_t *cand_key = sm.hist[1];
-    const bool once = run <= kQsMarked;
+    uint8_t *marks = sm.marks();
+    uint32_t *cand_key = sm.keys();
+    const bool once = run <= Smem::kMarked;
     bool marks_done = false, alone = false;
     const uint32_t others = (uint32_t)(c1 - c0 - max(0, min(c1, q.hi) - max(c0, q.lo)));       // not contested
     if (tid == 0) {
@@ -359,7 +384,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
     auto each_cand = [&](int upto, auto &&f) {
         uint32_t most = 0;
         for (int w = 0; w < upto; w++) most = max(most, sm.all[w]);
-        for (uint32_t i = tid; i < most; i += kQsThreads) {
+        for (uint32_t i = tid; i < most; i += NT) {
             uint32_t k[kQeMaxCluster];
 #pragma unroll
             for (int w = 0; w < kQeMaxCluster; w++) k[w] = w < upto && i < sm.all[w] ? cluster.map_shared_rank(cand_key, w)[i] : 0u;
@@ -375,7 +400,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         for (int d = 0; d < 3; d++) {
             const Digit g = digit_of(d);
             const int copies = d == 0 ? kQsCopies : 1;
-            for (int i = tid; i < copies * kQeBins; i += kQsThreads) sm.hist[0][i] = 0;
+            for (int i = tid; i < copies * kQeBins; i += NT) sm.hist[0][i] = 0;
             __syncthreads();
             // the contested part of the run, from a multiple of 4 on
             const int first = max(c0, q.lo), end = min(c1, q.hi);
@@ -424,9 +449,9 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                     const int e = __ffs(c) - 1;
                     const uint32_t k = weight_key(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3]), at = atomicAdd(&sm.cands, 1u);
                     atomicAdd(&hist[(k >> g.shift) & (g.bins - 1)], 1u);
-                    if (at < kQsCands) {
+                    if (at < Smem::kCands) {
                         cand_key[at] = k;
-                        sm.cand[at] = (uint16_t)(i + e - c0);
+                        sm.cand[at] = i + e - c0;
                     }
                 }
             };
@@ -435,14 +460,14 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             } else if (d == 1 && once) {
                 each(c0, c1, count_and_mark);
             } else if (marks_done) {
-                for (int i = tid; i < (int)sm.cands; i += kQsThreads)
+                for (int i = tid; i < (int)sm.cands; i += NT)
                     if ((cand_key[i] & g.above) == prefix) atomicAdd(&hist[(cand_key[i] >> g.shift) & (g.bins - 1)], 1u);
             } else {
                 each(first / 4 * 4, end, count);
             }
             if (d == 0) {
                 __syncthreads();
-                for (int i = tid; i < kQeBins; i += kQsThreads) {
+                for (int i = tid; i < kQeBins; i += NT) {
                     uint32_t v = 0;
 #pragma unroll
                     for (int w = 0; w < kQsCopies; w++) v += sm.hist[w][i];
@@ -459,20 +484,20 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                 __syncthreads();
                 uint32_t total = 0, most = 0;
                 for (int w = 0; w < ranks; w++) total += sm.all[w], most = max(most, sm.all[w]);
-                alone = most <= kQsCands && total <= kQsShared;
+                alone = most <= Smem::kCands && total <= kQsShared;
             }
             if (alone) {                 // the other digits without the other CTAs' help
                 marks_done = true;
 #pragma unroll 1
                 for (int e = 1; e < 3; e++) {
                     const Digit h = digit_of(e);
-                    for (int i = tid; i < h.bins; i += kQsThreads) sm.sums[i] = 0;
+                    for (int i = tid; i < h.bins; i += NT) sm.sums[i] = 0;
                     __syncthreads();
                     each_cand(ranks, [&](uint32_t k) {
                         if ((k & h.above) == prefix) atomicAdd(&sm.sums[(k >> h.shift) & (h.bins - 1)], 1u);
                     });
                     __syncthreads();
-                    find_digit<kQsThreads>(sm.sums, h.bins, sm.ws, left, &sm.digit, &sm.left);
+                    find_digit<NT>(sm.sums, h.bins, sm.ws, left, &sm.digit, &sm.left);
                     prefix |= sm.digit << h.shift;
                     left = sm.left;
                     __syncthreads();
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             }
             // each CTA joins the counts of its share of the bins and gives all the sums
             const int share = g.bins / ranks;
-            for (int i = tid; i < share; i += kQsThreads) {
+            for (int i = tid; i < share; i += NT) {
                 uint32_t x[kQeMaxCluster], v = 0;
 #pragma unroll
                 for (int w = 0; w < kQeMaxCluster; w++) x[w] = w < ranks ? cluster.map_shared_rank(sm.hist[0], w)[rank * share + i] : 0u;
@@ -492,20 +517,20 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
                     if (w < ranks) cluster.map_shared_rank(sm.sums, w)[rank * share + i] = v;
             }
             cluster.sync();
-            find_digit<kQsThreads>(sm.sums, g.bins, sm.ws, left, &sm.digit, &sm.left);
+            find_digit<NT>(sm.sums, g.bins, sm.ws, left, &sm.digit, &sm.left);
             const uint32_t digit = sm.digit;
             prefix |= digit << g.shift;
             left = sm.left;
-            for (int i = tid; i < g.bins; i += kQsThreads)
+            for (int i = tid; i < g.bins; i += NT)
                 if (i > (int)digit) own += sm.hist[0][i];
             if (d == 2) ties = sm.hist[0][digit];
-            if (d == 1) marks_done = once && sm.cands <= kQsCands;
+            if (d == 1) marks_done = once && sm.cands <= Smem::kCands;
             __syncthreads();
         }
         if (marks_done)                  // the other slots that stay or tie
-            for (int i = tid; i < (int)sm.cands; i += kQsThreads) {
+            for (int i = tid; i < (int)sm.cands; i += NT) {
                 const uint32_t k = cand_key[i], j = sm.cand[i];
-                if (k >= prefix) atomicOr(&sm.hist[3][j >> 4], 1u << (8 * (j >> 2 & 3) + (j & 3) + (k == prefix ? 4 : 0)));
+                if (k >= prefix) atomicOr(reinterpret_cast<uint32_t *>(marks) + (j >> 4), 1u << (8 * (j >> 2 & 3) + (j & 3) + (k == prefix ? 4 : 0)));
             }
     }
     // kept slots before this CTA's
@@ -543,10 +568,10 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         cluster.barrier_arrive();
     }
     int *list = kept_list(a, p);
-    uint16_t *chunk = reinterpret_cast<uint16_t *>(sm.sums);     // which other CTAs no longer read (nor hist[0])
+    uint16_t *chunk = sm.chunk();
     const bool nan = prefix == 0;                    // the threshold is NaN: all others are above it
     const float limit = nan ? 0.0f : key_weight(prefix);
-    for (int c = c0; c < c1; c += kQsChunk) {
+    for (int c = c0; c < c1; c += 32 * NT) {
         auto mark = [&](const float x[4], int i) {
             uint32_t keep = 0, tie = 0;
 #pragma unroll
@@ -558,13 +583,13 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
             }
             marks[(i - c) >> 2] = (uint8_t)(keep | tie << 4);
         };
-        const int stop = min(c1, c + kQsChunk);
+        const int stop = min(c1, c + 32 * NT);
         if (!marks_done) each(c, stop, mark);
         __syncthreads();
         uint32_t keep, tie, total;
         const int i0 = c + 32 * tid;
         marked(marks + (marks_done ? (c - c0) / 4 : 0) + 8 * tid, stop - i0, &keep, &tie);
-        const uint32_t scan = block_excl_scan<kQsThreads>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
+        const uint32_t scan = block_excl_scan<NT>(__popc(keep) << 16 | __popc(tie), sm.ws, &total);
         uint32_t rest = ties_before + (scan & 0xffffu), at = (scan >> 16) + min(rest, left) - min(ties_before, left);
         const int kept = (int)((total >> 16) + min(ties_before + (total & 0xffffu), left) - min(ties_before, left));
         ties_before += total & 0xffffu;
@@ -574,7 +599,7 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         } else {
             for (; keep; keep &= keep - 1) chunk[at++] = (uint16_t)(32 * tid + __ffs(keep) - 1);
             __syncthreads();
-            for (int j = 32 * warp; j < kept; j += kQsThreads) {
+            for (int j = 32 * warp; j < kept; j += NT) {
                 const int m = min(32, kept - j);
                 move_rows(a, p, lane < m ? c + chunk[j + lane] : 0, m, before + j, false);
             }
@@ -582,18 +607,30 @@ __global__ void __launch_bounds__(kQsThreads, 4) k_quant_select(QuantEvictArgs a
         __syncthreads();                             // the marks and the list have been read
         before += kept;
     }
-    finish(a, p, q.n, kQsThreads);
+    finish(a, p, q.n, NT);
     cluster.barrier_wait();                          // and this CTA's by the others
 }
 
+__global__ void __launch_bounds__(kQsMany, 4) k_quant_select(QuantEvictArgs a)
+{
+    __shared__ QsSmem<kQsMany> sm;
+    quant_select(a, sm);
+}
+
+__global__ void __launch_bounds__(kQsFew, 1) k_quant_select_few(QuantEvictArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    quant_select(a, *reinterpret_cast<QsSmem<kQsFew> *>(smem_raw));
+}
+
 // Rows of the listed slots, a warp 32 of them.
-__global__ void __launch_bounds__(kQsThreads) k_quant_gather(QuantEvictArgs a)
+__global__ void __launch_bounds__(kQgThreads) k_quant_gather(QuantEvictArgs a)
 {
     const int p = blockIdx.y, lane = threadIdx.x & 31;
     pdl_wait();
     const int kept = (int)min((int64_t)quant_len(a.src, p), a.budget);
     const int *list = kept_list(a, p);
-    const int64_t j = (int64_t)blockIdx.x * kQsThreads + (threadIdx.x & ~31);
+    const int64_t j = (int64_t)blockIdx.x * kQgThreads + (threadIdx.x & ~31);
     if (j >= kept) return;
     const int m = min(32, kept - (int)j);
     move_rows(a, p, lane < m ? list[j + lane] : 0, m, j, false);
@@ -615,10 +652,21 @@ cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
         return launch_pdl(k_quant_evict, dim3(c, a.src.bh), dim3(kQeThreads), sizeof(QeSmem), s, a);
     }
     // more while there is room for all at once and four slots for each thread
-    while (c < kQeMaxCluster && 2 * c * a.src.bh <= 4 * sms && a.src.n_cap >= 2 * c * 4 * kQsThreads) c *= 2;
+    // a cluster of large CTAs needs 8 SMs of one part of the GPU: up to 12 pairs are all there at once (16 pairs of
+    // 262144 keys: 64 us for 50); fewer slots than 12 a thread do not pay (1 pair of 40007 keys: 24 us for 22, of 131072
+    // 25.7 for 26.4)
+    const bool few = 12 * a.src.bh <= sms && a.src.n_cap >= (int64_t)kQeMaxCluster * 12 * kQsFew;
+    while (c < kQeMaxCluster && (few || 2 * c * a.src.bh <= 4 * sms) && a.src.n_cap >= 2 * c * 4 * kQsMany) c *= 2;
+    const int smem = few ? (int)sizeof(QsSmem<kQsFew>) : 0;
+    if (few) {
+        static std::atomic<int> done[kMaxDevices];
+        e = dyn_smem_limit(k_quant_select_few, smem, done);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c, a.src.bh);
-    cfg.blockDim = dim3(kQsThreads);
+    cfg.blockDim = dim3(few ? kQsFew : kQsMany);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -629,10 +677,10 @@ cudaError_t launch_quant_evict(const QuantEvictArgs &a, cudaStream_t s)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_quant_select, a);
+    e = cudaLaunchKernelEx(&cfg, few ? k_quant_select_few : k_quant_select, a);
     if (e != cudaSuccess || !(a.keep || a.dst.acc)) return e;
     const int64_t most = a.budget < a.src.n_cap ? a.budget : a.src.n_cap;
-    return launch_pdl(k_quant_gather, dim3((unsigned)((most + kQsThreads - 1) / kQsThreads), a.src.bh), dim3(kQsThreads), 0, s, a);
+    return launch_pdl(k_quant_gather, dim3((unsigned)((most + kQgThreads - 1) / kQgThreads), a.src.bh), dim3(kQgThreads), 0, s, a);
 }
 
 }  // namespace pk

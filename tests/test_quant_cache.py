@@ -567,11 +567,11 @@ def test_evict_sizes_at_the_borders(pk, n, cap, shift):
 
 
 @gpu
-@pytest.mark.parametrize("n", [131104, 270000, 40000])
+@pytest.mark.parametrize("bh,n", [(20, 131104), (2, 270000), (20, 40000), (2, 131104), (1, 1048576), (1, 2100000), (17, 290001)])
 @pytest.mark.parametrize("kind", ["equal", "few", "part", "near", "nan", "inf"])
-def test_evict_crowded_weights(pk, n, kind):
+def test_evict_crowded_weights(pk, bh, n, kind):
     """Weights that agree in their first bits: everywhere, in a part of the slots, or in all but the last bits."""
-    bh, budget, sink, recent = 2, 2500, 7, 33
+    budget, sink, recent = 2500, 7, 33
     cap = -(-n // KEYS) * KEYS
     g = torch.Generator(device="cuda").manual_seed(n)
     acc = torch.rand(bh, cap, generator=g, device="cuda")
