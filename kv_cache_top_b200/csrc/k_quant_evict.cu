@@ -52,7 +52,7 @@ static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots")
 // 1024 where each has an SM for itself: four times the loads in flight, and
 // room for the marks of a longer run (4 pairs of 1048576 keys: 56 us
 // for 122).
-constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (66 us for 50)
+constexpr int kQsCopies = 4;             // of the first digit's counts: weights crowd in few bins (one copy: 66 us, four: 50)
 constexpr int kQsMany = 256, kQsFew = 1024;
 template <int NT>
 struct QsState {
