@@ -75,6 +75,32 @@ __device__ __forceinline__ Raw8 load8(const void *p, int64_t i, int vec)
     return x;
 }
 
+// the 32 channels of a group
+template <bool BF16>
+__device__ __forceinline__ void load_group(Raw8 x[4], const void *p, int64_t i, int vec)
+{
+    if (vec < 32) {
+#pragma unroll
+        for (int c = 0; c < 4; c++) x[c] = load8<BF16>(p, i + 8 * c, vec);
+        return;
+    }
+    // 32 bytes at once: by 16 each sector would be asked for twice (32768 rows of 8 pairs: 30 us alone, 37)
+    const uint8_t *b = reinterpret_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int c = 0; c < (BF16 ? 2 : 4); c++) {
+        uint32_t w[8];
+        asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(b + 32 * c)
+                     : "memory");
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            if (BF16) x[2 * c + e / 4].w[e % 4] = w[e];
+            else x[c].w[e] = w[e];
+        }
+    }
+}
+
 // The codes of a group's 32 channels (x[i].. : channels 8i .. 8i + 7) and its
 // scale bits.  K: word i has channels 8i + e as nibbles e; V: word e / 2 has
 // channels 8i + e as nibbles 4 (e % 2) + i.
@@ -198,7 +224,9 @@ __device__ __forceinline__ uint32_t spread_nibbles(uint32_t x)
 template <bool BF16>
 __global__ void __launch_bounds__(kQrThreads, BF16 ? 6 : 3) k_quant_append(QuantRowsArgs a, int tiles)
 {
-    __shared__ __align__(16) uint8_t img[kQBlock];
+    // rows 80 bytes apart: the stores of 8 rows meet in fewer banks
+    __shared__ __align__(16) uint8_t img[2][kQKeys][kQRow + 16];
+    __shared__ __align__(16) uint16_t scale[2][kQKeys][4];
     const int p = blockIdx.y, tid = threadIdx.x;
     pdl_wait();
     const int64_t at = a.at ? a.at[p] : a.c.lens[p];
@@ -213,26 +241,24 @@ __global__ void __launch_bounds__(kQrThreads, BF16 ? 6 : 3) k_quant_append(Quant
             const bool values = tid >= 4 * kQKeys;
             Raw8 x[4];
             uint32_t w[4], sb;
-#pragma unroll
-            for (int i = 0; i < 4; i++) x[i] = load8<BF16>(values ? a.v : a.k, base + 8 * i, a.vec);
+            load_group<BF16>(x, values ? a.v : a.k, base, a.vec);
             if (values) {
                 quant_group<BF16, true>(x, w, &sb);
-                uint8_t *row = img + kQOffV + j * kQRow + 2 * r;
+                uint8_t *row = img[1][j] + 2 * r;
 #pragma unroll
                 for (int g = 0; g < 8; g++) *reinterpret_cast<uint16_t *>(row + 8 * (g ^ v_turn(j))) = (uint16_t)(w[g >> 1] >> (16 * (g & 1)));
             } else {
                 quant_group<BF16, false>(x, w, &sb);
 #pragma unroll
-                for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t *>(img + j * kQRow + 16 * i + 4 * r) = w[i];
+                for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t *>(img[0][j] + 16 * i + 4 * r) = w[i];
             }
-            *reinterpret_cast<uint16_t *>(img + (values ? kQOffVs : kQOffKs) + 8 * j + 2 * r) = (uint16_t)sb;
+            scale[values][j][r] = (uint16_t)sb;
         }
         __syncthreads();
         uint8_t *dst = a.c.blocks + ((int64_t)p * (a.c.n_cap / kQKeys) + b) * kQBlock;
-        const int o = tid & 127, off = tid >> 7 ? kQOffV : 0;
-        if (o >= 4 * j0 && o < 4 * j1) reinterpret_cast<uint4 *>(dst + off)[o] = reinterpret_cast<const uint4 *>(img + off)[o];
+        if (j >= j0 && j < j1) reinterpret_cast<uint4 *>(dst + (tid >> 7 ? kQOffV : 0))[tid & 127] = reinterpret_cast<const uint4 *>(img[tid >> 7][j])[r];
         if (tid < 2 * kQKeys && (tid & 31) >= j0 && (tid & 31) < j1)
-            reinterpret_cast<uint2 *>(dst + kQOffKs)[tid] = reinterpret_cast<const uint2 *>(img + kQOffKs)[tid];
+            reinterpret_cast<uint2 *>(dst + kQOffKs)[tid] = reinterpret_cast<const uint2 *>(scale)[tid];
         if (a.c.acc && tid >= j0 && tid < j1) a.c.acc[(int64_t)p * a.c.n_cap + b * kQKeys + tid] = 0.0f;
         if (gridDim.x < tiles) __syncthreads();
     }

@@ -59,6 +59,13 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
+// bytes on whose boundary two arrays' rows lie
+int32_t row_boundary(const void *a, const void *b)
+{
+    const uintptr_t x = (uintptr_t)a | (uintptr_t)b;
+    return x % 32 == 0 ? 32 : x % 16 == 0 ? 16 : 0;
+}
+
 // bytes of the partial results, a multiple of 256
 size_t part_bytes(int32_t bh, int32_t G)
 {
@@ -93,7 +100,7 @@ pk_status pk_quant_append(const pk_quant_cache *cache, const void *k_new, const 
     a.at = at;
     a.own_at = at && !meets;
     a.is_bf16 = cache->kv_dtype == PK_BF16;
-    a.vec = (uintptr_t)k_new % 16 == 0 && (uintptr_t)v_new % 16 == 0;
+    a.vec = row_boundary(k_new, v_new);
     return quant_status(launch_quant_append(a, (cudaStream_t)stream));
 }
 
@@ -113,7 +120,7 @@ pk_status pk_quant_rows(const pk_quant_cache *cache, int64_t n_rows, void *k_out
     a.stride = n_rows;
     a.at = at;
     a.is_bf16 = cache->kv_dtype == PK_BF16;
-    a.vec = (uintptr_t)k_out % 16 == 0 && (uintptr_t)v_out % 16 == 0;
+    a.vec = row_boundary(k_out, v_out);
     return quant_status(launch_quant_rows(a, (cudaStream_t)stream));
 }
 

@@ -54,7 +54,7 @@ struct QuantRowsArgs {
     const int32_t *at;       // first slot per pair, or null
     int32_t own_at;          // append: `at` does not overlap the lengths
     int32_t is_bf16;
-    int32_t vec;             // rows are 16-byte aligned
+    int32_t vec;             // bytes on whose boundary the rows lie: 32, 16 or 0 (less)
 };
 
 // Attention splits the pairs' blocks, laid end to end, over the CTAs
