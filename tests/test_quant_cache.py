@@ -238,6 +238,35 @@ def test_append_extreme_values(pk):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top", [1.0, 2.0 ** 126, 2.0 ** -56, 2.0 ** -57, 2.0 ** -58, 2.0 ** -126])
+def test_append_every_bf16_value_of_a_group(pk, dtype, top):
+    """Every bf16 value between a group's largest, of every mantissa, and its 64th part: all codes, borders and ties."""
+    td, kind = dt(pk, dtype)
+    big = np.float32(top) * (1 + np.arange(128, dtype=np.float32) / 128)
+    steps = np.concatenate([np.float32(2.0 ** -e) * (1 + np.arange(128, dtype=np.float32) / 128) for e in range(7)])
+    groups = []
+    for m in big:
+        x = np.float32(top) * steps
+        x = np.sort(x[x <= m])[::-1] * np.where(np.arange((x <= m).sum()) % 2, -1, 1).astype(np.float32)
+        x = np.concatenate([x, np.zeros(-len(x) % 31, np.float32)]).reshape(-1, 31)
+        groups.append(np.concatenate([np.full((len(x), 1), m, np.float32), x], 1))
+    g = np.concatenate(groups)
+    g = np.concatenate([g, np.zeros((-len(g) % 4, 32), np.float32)])
+    rows = torch.from_numpy(g.reshape(-1, D)).to(td)
+    n = len(rows)
+    cap = -(-n // KEYS) * KEYS
+    c, _ = make_cache(pk, np.random.default_rng(0), [0], cap, kind)
+    pk.pk_quant_append(c, rows.cuda()[None], rows.flip(0).contiguous().cuda()[None], n)
+    kc, vc, ks, vs = ref.decode(c.tensors[0][0].cpu().numpy())
+    for code, s, x in ((kc, ks, rows), (vc, vs, rows.flip(0))):
+        want, scale, _ = ref.stored(x.float().numpy())
+        assert np.array_equal(s[:n], scale)
+        live = np.repeat(scale > 0, 32, 1)
+        assert np.array_equal(code[:n][live], want[live])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_append_at_places_and_refuses_what_does_not_fit(pk, dtype):
     td, kind = dt(pk, dtype)
     for n_new in (3, 70):                # one CTA per pair, several
