@@ -633,12 +633,51 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     if (late && lane == 0 && a.c.status && atomicCAS(a.c.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.c.status[1] = p;
 }
 
+// One channel of a head's output and the head's log-sum from its ns partial
+// results at pg, N at a time, all that is needed of them in flight at once:
+// every thread sums the head's weights too, one round trip to memory instead of
+// two and a barrier (64 ragged pairs: 33 us for 35).  More than 6 at a time cost
+// more instructions than they save in latency (8 pairs of 18 partial results:
+// 24.2 us, 24.7 by 8, 25.8 by 18; 256 pairs of 2: 20.0 us, 22.5 by 8).
+template <int N>
+__device__ __forceinline__ float2 merge_parts(const float *pg, int64_t stride, int ns, int c)
+{
+    float top = -INFINITY, l = 0.0f, o = 0.0f, ref = 0.0f;
+    for (int s = 0; s < ns; s += N) {
+        float m[N], w[N], x[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float *q = pg + (s + i) * stride;
+            const bool in = s + i < ns;
+            m[i] = in ? q[kD] : -INFINITY;
+            w[i] = in ? q[kD + 1] : 0.0f;
+            x[i] = in ? q[c] : 0.0f;
+        }
+        const float old = top;
+#pragma unroll
+        for (int i = 0; i < N; i++) top = fmaxf(top, m[i]);
+        ref = top == -INFINITY ? 0.0f : top;
+        const float down = ex2(old - ref);
+        l *= down;
+        o *= down;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float f = ex2(m[i] - ref);
+            l = fmaf(f, w[i], l);
+            o = fmaf(f, x[i], o);
+        }
+    }
+    return make_float2(l == 0.0f ? 0.0f : o / l, (log2f(l) + ref) * 0.69314718055994531f);
+}
+
 // Merge of a pair's partial results (the first a.outs CTAs) and its part of acc
 // (the others, kQmKeys keys each).  The lengths are read before the attention
 // kernel has ended: it waited for whatever wrote them.
-__global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
+template <bool WIDE>
+__global__ void __launch_bounds__(kQmThreads, WIDE ? 3 : 4) k_quant_merge(QuantAttendArgs a)
 {
-    __shared__ float s_ref[kMaxGroup], s_l[kMaxGroup], s_lse[kMaxGroup];
+    constexpr int kHeads = WIDE ? kMaxGroup : 4;
+    __shared__ float s_lse[kHeads];
     const int tid = threadIdx.x, p = blockIdx.y, G = a.G;
     const int n = quant_len(a.c, p);
     const int outs = a.outs;
@@ -652,13 +691,58 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
         if (blockIdx.x == 0 && tid < G && a.lse) a.lse[(int64_t)p * G + tid] = -INFINITY;
         return;
     }
-    const uint2 at = a.parts[p];         // the pair's partial results: slots p + at.x .. p + at.x + at.y - 1
-    const int ns = (int)at.y;
-    const float *part = a.part + (int64_t)(p + at.x) * G * kQPart;
+    const uint2 *parts = a.parts + p;    // slots p + x .. p + x + y - 1 have the pair's partial results
     const int warp = tid >> 5, lane = tid & 31;
     const int64_t stride = (int64_t)G * kQPart;
-    if (warp < G) {                      // head `warp`: its reference, sum and log-sum
-        const float *pg = part + warp * kQPart + kD;
+    if (is_out) {
+        const uint2 at = *parts;
+        const int ns = (int)at.y;
+        for (int e = (int)blockIdx.x * kQmThreads + tid; e < G * kD; e += outs * kQmThreads) {
+            const float *pg = a.part + (int64_t)(p + at.x) * stride + e / kD * kQPart;
+            const float2 v = ns <= 2 ? merge_parts<2>(pg, stride, ns, e % kD) : merge_parts<6>(pg, stride, ns, e % kD);
+            a.out[(int64_t)p * G * kD + e] = v.x;
+            if (e % kD == 0 && a.lse) a.lse[(int64_t)p * G + e / kD] = v.y;
+        }
+        return;
+    }
+    // 4 keys a thread: all heads' logits and the sums in flight at once, the first ones beside the log-sums'
+    float *acc = a.c.acc + (int64_t)p * a.c.n_cap;
+    const bool vec = (uintptr_t)acc % 16 == 0;
+    const int64_t end = min((int64_t)n, k0 + kQmKeys);
+    auto load = [&](int64_t k, float4 x[kHeads], float4 *sum) {
+        const float *z = a.logits + ((int64_t)p * (a.c.n_cap / kQKeys) + k / kQKeys) * G * kQKeys + k % kQKeys;
+#pragma unroll
+        for (int g = 0; g < kHeads; g++)
+            if (g < G) x[g] = __ldcs(reinterpret_cast<const float4 *>(z + g * kQKeys));
+        if (vec && k + 4 <= n) *sum = *reinterpret_cast<const float4 *>(acc + k);
+    };
+    auto add = [&](int64_t k, const float4 x[kHeads], const float4 &sum) {
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int g = 0; g < kHeads; g++)
+            if (g < G) {
+                const float lse = s_lse[g];
+                w.x += ex2(x[g].x - lse);
+                w.y += ex2(x[g].y - lse);
+                w.z += ex2(x[g].z - lse);
+                w.w += ex2(x[g].w - lse);
+            }
+        if (vec && k + 4 <= n) {
+            *reinterpret_cast<float4 *>(acc + k) = make_float4(sum.x + w.x, sum.y + w.y, sum.z + w.z, sum.w + w.w);
+        } else {
+            acc[k] += w.x;
+            if (k + 1 < n) acc[k + 1] += w.y;
+            if (k + 2 < n) acc[k + 2] += w.z;
+            if (k + 3 < n) acc[k + 3] += w.w;
+        }
+    };
+    float4 x[kHeads], sum;
+    int64_t k = k0 + 4 * tid;
+    if (k < end) load(k, x, &sum);
+    if (warp < G) {                      // head `warp`: its log-sum
+        const uint2 at = *parts;
+        const int ns = (int)at.y;
+        const float *pg = a.part + (int64_t)(p + at.x) * stride + warp * kQPart + kD;
         float m = -INFINITY;
         for (int s = lane; s < ns; s += 32) m = fmaxf(m, pg[s * stride]);
 #pragma unroll
@@ -668,57 +752,14 @@ __global__ void __launch_bounds__(kQmThreads) k_quant_merge(QuantAttendArgs a)
         for (int s = lane; s < ns; s += 32) l += ex2(pg[s * stride] - ref) * pg[s * stride + 1];
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-        if (lane == 0) {
-            s_ref[warp] = ref;
-            s_l[warp] = l;
-            s_lse[warp] = l == 0.0f ? INFINITY : log2f(l) + ref;
-            if (blockIdx.x == 0 && a.lse) a.lse[(int64_t)p * G + warp] = (log2f(l) + ref) * 0.69314718055994531f;
-        }
+        if (lane == 0) s_lse[warp] = l == 0.0f ? INFINITY : log2f(l) + ref;
     }
-    static_assert(kQmThreads / 32 >= kMaxGroup, "a warp for each head");
+    static_assert(kQmThreads / 32 >= kHeads, "a warp for each head");
     __syncthreads();
-    if (is_out) {
-        for (int e = (int)blockIdx.x * kQmThreads + tid; e < G * kD; e += outs * kQmThreads) {
-            const int g = e / kD;
-            const float *pg = part + g * kQPart, ref = s_ref[g], l = s_l[g];
-            float o = 0.0f;
-#pragma unroll 8
-            for (int s = 0; s < ns; s++) o = fmaf(ex2(pg[s * stride + kD] - ref), pg[s * stride + e % kD], o);
-            a.out[(int64_t)p * G * kD + e] = l == 0.0f ? 0.0f : o / l;
-        }
-        return;
-    }
-    // 4 keys a thread: all heads' logits and the sums in flight at once
-    float *acc = a.c.acc + (int64_t)p * a.c.n_cap;
-    const bool vec = (uintptr_t)acc % 16 == 0;
-#pragma unroll 2
-    for (int64_t k = k0 + 4 * tid; k < min((int64_t)n, k0 + kQmKeys); k += 4 * kQmThreads) {
-        const float *z = a.logits + ((int64_t)p * (a.c.n_cap / kQKeys) + k / kQKeys) * G * kQKeys + k % kQKeys;
-        float4 x[kMaxGroup];
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; g++)
-            if (g < G) x[g] = __ldcs(reinterpret_cast<const float4 *>(z + g * kQKeys));
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const bool whole = vec && k + 4 <= n;
-        if (whole) sum = *reinterpret_cast<const float4 *>(acc + k);
-        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; g++)
-            if (g < G) {
-                const float lse = s_lse[g];
-                w.x += ex2(x[g].x - lse);
-                w.y += ex2(x[g].y - lse);
-                w.z += ex2(x[g].z - lse);
-                w.w += ex2(x[g].w - lse);
-            }
-        if (whole) {
-            *reinterpret_cast<float4 *>(acc + k) = make_float4(sum.x + w.x, sum.y + w.y, sum.z + w.z, sum.w + w.w);
-        } else {
-            acc[k] += w.x;
-            if (k + 1 < n) acc[k + 1] += w.y;
-            if (k + 2 < n) acc[k + 2] += w.z;
-            if (k + 3 < n) acc[k + 3] += w.w;
-        }
+    while (k < end) {
+        add(k, x, sum);
+        k += 4 * kQmThreads;
+        if (k < end) load(k, x, &sum);
     }
 }
 
@@ -740,7 +781,7 @@ cudaError_t launch_quant_attend(const QuantAttendArgs &args, int num_sms, cudaSt
     const unsigned parts = a.accumulate ? (unsigned)((a.c.n_cap + kQmKeys - 1) / kQmKeys) : 0u;
     // few pairs have many partial results each: one pass a CTA; many have few: fewer CTAs (256 pairs: 22 us for 24)
     a.outs = a.c.bh < num_sms ? (a.G + kQmHeads - 1) / kQmHeads : 1;
-    return launch_pdl(k_quant_merge, dim3(a.outs + parts, a.c.bh), dim3(kQmThreads), 0, s, a);
+    return launch_pdl(a.G > 4 ? k_quant_merge<true> : k_quant_merge<false>, dim3(a.outs + parts, a.c.bh), dim3(kQmThreads), 0, s, a);
 }
 
 }  // namespace pk
