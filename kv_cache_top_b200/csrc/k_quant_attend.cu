@@ -32,6 +32,10 @@ constexpr int kQmThreads = 256;          // merge kernel
 constexpr int kQmKeys = 2048;            // keys of a merge CTA's part of acc
 constexpr int kQmHeads = kQmThreads / kD;      // heads whose outputs are one pass of a merge CTA
 
+struct Place {
+    uint32_t pair, first, start, end;    // blocks start .. end - 1 of all; the pair of the first, and that pair's first
+};
+
 struct QaSmem {
     uint8_t ring[kQaWarps][kQaStages][kQBlock];
     unsigned long long bar[kQaWarps][kQaStages];
@@ -42,9 +46,9 @@ struct QaSmem {
     float qscale[kQaGroups][2][kMaxGroup];
     uint32_t ws[kQaWarps + 1];
     float factor[kQaWarps][8];           // of a warp's column in the segment's sums
-    uint32_t pair[kQaGroups], first[kQaGroups], start[kQaGroups], end[kQaGroups];
-    int by_pairs;
-    uint32_t share;
+    uint32_t fits[kQaWarps];
+    Place place[kQaGroups];
+    uint32_t share[kQaGroups];           // blocks a worker takes; by pairs: bit 31 (for the thread that writes it)
     int has[kQaWarps];
     alignas(16) uint32_t q[kQaGroups][2][kMaxGroup][4][4][8];      // last: as many workers as the CTA has; [worker][segment parity][head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
 };
@@ -82,19 +86,28 @@ __device__ __forceinline__ uint32_t ceil_share(uint32_t nb, uint32_t share, floa
     return q + (r > 0);
 }
 
+// Blocks a worker takes of `total` cut evenly.
+__device__ __forceinline__ uint32_t even_share(uint32_t total, int workers, int span)
+{
+    return max((total + (uint32_t)workers - 1) / (uint32_t)workers, (uint32_t)min_share(span));
+}
+
 // Up to 32 PER pairs, and no more than workers: a worker takes blocks of one
 // pair only, `share` of them, the smallest that does with the workers there
-// are, unless that is more than an even share by over a round of the warps,
+// are, unless that is more than an even share by about a round of the warps,
 // what a second merge costs (64 ragged pairs of up to 282 blocks: 35 us by
 // pairs, 55 evenly; 64 pairs of 4096 blocks, 2 workers for each and 20 idle:
-// 300 and 268).  Else the pairs' blocks are laid end to end and cut evenly.  By
-// one warp: the share, or 0 for even ones; nb[i] is the block count of pair
-// lane + 32 i.
-template <int PER>
-__device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers, int span, int lane, uint32_t nb[PER])
+// 300 and 268).  Else (the result is 0) the pairs' blocks are laid end to end
+// and cut evenly.  The share, and the place of `worker` (end 0: no work): warp w
+// tries the share w above the even one, and every warp places its worker for
+// itself (8 pairs of 32768 keys: 22.6 us; by one warp, with a search and a
+// broadcast: 24.3).
+template <int PER, int SPAN>
+__device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers, uint32_t worker, int warp, int lane, uint32_t *fits, Place *at)
 {
+    *at = Place{0u, 0u, 0u, 0u};
     if (c.bh > 32 * PER || c.bh > workers) return 0;
-    uint32_t total = 0;
+    uint32_t nb[PER], total = 0;         // nb[i]: block count of pair lane + 32 i
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int p = lane + 32 * i;
@@ -102,62 +115,47 @@ __device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers,
         total += nb[i];
     }
     total = __reduce_add_sync(kFull, total);
-    auto need = [&](uint32_t share) {    // workers at this share
-        const float inv = 1.0f / (float)share;
-        uint32_t k = 0;
+    const uint32_t even = even_share(total, workers, SPAN);
+    {
+        const uint32_t share = even + warp;
+        const float inv = __frcp_rn((float)share);
+        uint32_t k = 0;                  // workers at this share
 #pragma unroll
         for (int i = 0; i < PER; i++)
             if (32 * i < c.bh) k += ceil_share(nb[i], share, inv);
-        return __reduce_add_sync(kFull, k);
-    };
-    uint32_t lo = (uint32_t)quant_share(total, workers, min_share(span)), hi = lo + span;
-    if (need(hi) > (uint32_t)workers) return 0;
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (need(mid) <= (uint32_t)workers) hi = mid;
-        else lo = mid + 1;
+        k = __reduce_add_sync(kFull, k);
+        if (lane == 0) fits[warp] = warp <= SPAN && k <= (uint32_t)workers;
     }
-    return hi;
-}
-
-// By pairs: the blocks of the workers worker0 .. of a CTA, by its first warp.
-template <int PER, int SPAN>
-__device__ __forceinline__ void place_workers(const QuantCache &c, int workers, uint32_t worker0, int lane, QaSmem &sm)
-{
-    constexpr int kGroups = kQaWarps / SPAN;
-    uint32_t nb[PER];
-    const uint32_t share = plan_pairs<PER>(c, workers, SPAN, lane, nb);
-    if (lane == 0) {
-        sm.by_pairs = share > 0;
-        sm.share = share;
-    }
-    if (lane < kGroups) sm.end[lane] = 0;        // no work unless a pair has some
-    __syncwarp();
-    if (share > 0) {
-        const float inv = 1.0f / (float)share;
-        uint32_t w0 = 0, f0 = 0;                 // workers and blocks of the pairs before
+    __syncthreads();
+    const uint32_t ok = __ballot_sync(kFull, lane < kQaWarps && fits[lane & (kQaWarps - 1)]);
+    if (ok == 0) return 0;
+    const uint32_t share = even + __ffs(ok) - 1;
+    const float inv = __frcp_rn((float)share);
+    uint32_t w0 = 0, f0 = 0;             // workers and blocks of the pairs before
 #pragma unroll
-        for (int i = 0; i < PER; i++) {
-            if (32 * i >= c.bh) break;
-            const uint32_t k = ceil_share(nb[i], share, inv);
-            uint32_t w = k, f = nb[i];
+    for (int i = 0; i < PER; i++) {
+        if (32 * i >= c.bh) break;
+        const uint32_t k = ceil_share(nb[i], share, inv);
+        uint32_t w = k, f = nb[i];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
-                if (lane >= o) w += x, f += y;
-            }
-            const uint32_t we = w0 + w, fe = f0 + f;         // ends of the lane's pair
-            for (uint32_t i0 = max(we - k, worker0); i0 < min(we, worker0 + kGroups); i0++) {
-                const int j = i0 - worker0;
-                sm.pair[j] = lane + 32 * i;
-                sm.first[j] = fe - nb[i];
-                sm.start[j] = fe - nb[i] + (i0 - (we - k)) * share;
-                sm.end[j] = min(fe, sm.start[j] + share);
-            }
-            w0 += __shfl_sync(kFull, w, 31);
-            f0 += __shfl_sync(kFull, f, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
+            if (lane >= o) w += x, f += y;
         }
+        const uint32_t we = w0 + w, first = f0 + f - nb[i];      // the lane's pair ends with worker we - 1
+        const uint32_t here = __ballot_sync(kFull, worker < we && worker >= we - k);
+        if (here) {
+            const int src = __ffs(here) - 1;
+            at->pair = src + 32 * i;
+            at->first = __shfl_sync(kFull, first, src);
+            at->start = at->first + (worker - __shfl_sync(kFull, we - k, src)) * share;
+            at->end = min(at->first + __shfl_sync(kFull, nb[i], src), at->start + share);
+            break;
+        }
+        w0 += __shfl_sync(kFull, w, 31);
+        f0 += __shfl_sync(kFull, f, 31);
     }
+    return share;
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -320,16 +318,17 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         if (SPAN == kQaWarps) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * SPAN) : "memory");
     };
-    if (warp == 0) {                     // each row of 32 pairs that is planned costs 0.1 us
-        if (a.c.bh <= 32) place_workers<1, SPAN>(a.c, a.workers, worker0, lane, sm);
-        else place_workers<SPAN == kQaWarps ? 4 : 8, SPAN>(a.c, a.workers, worker0, lane, sm);
-    }
-    __syncthreads();
-    if (!sm.by_pairs) {
+    Place at;
+    // each row of 32 pairs that is planned costs 0.1 us
+    uint32_t share = a.c.bh <= 32 ? plan_pairs<1, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at)
+                                  : plan_pairs<SPAN == kQaWarps ? 4 : 8, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at);
+    if (share > 0) {
+        share |= 0x80000000u;
+    } else {
         const uint32_t total = count_blocks(a.c, sm.ws);
-        const uint32_t share = (uint32_t)quant_share(total, a.workers, min_share(SPAN));
+        share = even_share(total, a.workers, SPAN);
         if (worker0 * share >= total) return;
-        if (tid == 0) sm.share = share;
+        if (tid < kGroups) sm.place[tid].end = 0;        // no work unless there are blocks for it
         for (uint32_t base = 0, c = 0;; c += kQaThreads) {
             const uint32_t v = c + tid < (uint32_t)a.c.bh ? block_count(a.c, c + tid) : 0u;
             uint32_t sum, last = 0;
@@ -338,10 +337,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             for (int j = 0; j < kGroups; j++) {
                 const uint32_t x = (worker0 + j) * share;
                 if (x >= before && x - before < v) {
-                    sm.pair[j] = c + tid;
-                    sm.first[j] = before;
-                    sm.start[j] = x;
-                    sm.end[j] = min(total, x + share);
+                    sm.place[j] = Place{c + tid, before, x, min(total, x + share)};
                 }
                 if (x < total) last = x;
             }
@@ -349,11 +345,13 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             if (base > last) break;
         }
         __syncthreads();
+        at = sm.place[group];
     }
-    const uint32_t x0 = sm.start[group], end = sm.end[group];
+    const uint32_t x0 = at.start, end = at.end;
     if (end == 0) return;
-    int p = (int)sm.pair[group];
-    uint32_t first = sm.first[group];    // first block of pair p
+    if (mate == 0 && lane == 0) sm.share[group] = share;
+    int p = (int)at.pair;
+    uint32_t first = at.first;           // first block of pair p
     const int64_t pair_blocks = a.c.n_cap / kQKeys;
 
     // the warp's blocks are x = mate (mod SPAN); copies run ahead of x
@@ -369,8 +367,6 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         if (lane == 0) fetch_block(sm.ring[warp][s], a.c.blocks + (fp * pair_blocks + (fx - ffirst)) * kQBlock, &sm.bar[warp][s]);
         fx += SPAN;
     };
-#pragma unroll 1
-    for (int s = 0; s < kQaStages; s++) fetch(s);
     int slot = 0;
     uint32_t parity = 0;
     bool late = false;
@@ -395,7 +391,9 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             if (h < G) stage_q(qv[i], a.scale2, sm.q[group][turn][h], &sm.qscale[group][turn][h], lane);
         }
     };
-    bring_q(p);
+    bring_q(p);                          // ahead of the copies, which fill the memory's queues
+#pragma unroll 1
+    for (int s = 0; s < kQaStages; s++) fetch(s);
     put_q(0);
     sync();
     int turn = 0;
@@ -403,8 +401,10 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         const int n = quant_len(a.c, p);
         const uint32_t nb = (uint32_t)(n + kQKeys - 1) / kQKeys, stop = min(end, first + nb);
         const bool has = x < stop;
-        if (first >= x0 && mate == 0 && lane == 0)   // this worker has the pair's first block: where its partial results are
-            a.parts[p] = make_uint2(worker, (sm.by_pairs ? (nb + sm.share - 1) / sm.share : (first + nb - 1) / sm.share - worker + 1));
+        if (first >= x0 && mate == 0 && lane == 0) { // this worker has the pair's first block: where its partial results are
+            const uint32_t share = sm.share[group] & 0x7fffffffu;
+            a.parts[p] = make_uint2(worker, sm.share[group] >> 31 ? (nb + share - 1) / share : (first + nb - 1) / share - worker + 1);
+        }
         float2 o[4][4];                  // channels 32r + {0, 16, 8, 24} + g, heads 2t and 2t + 1
         float m = -INFINITY;
         float2 l2 = make_float2(0.0f, 0.0f);

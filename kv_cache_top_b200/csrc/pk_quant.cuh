@@ -84,14 +84,6 @@ struct QuantEvictArgs {
     int32_t *keep;           // [bh][budget] or null
 };
 
-// Blocks per worker for `total` blocks cut evenly, at least `least`; used alike
-// by the attention kernel and its merge.
-__host__ __device__ __forceinline__ int64_t quant_share(int64_t total, int workers, int least)
-{
-    const int64_t s = (total + workers - 1) / workers;
-    return s > least ? s : least;
-}
-
 cudaError_t launch_quant_append(const QuantRowsArgs &a, cudaStream_t s);
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t s);
 cudaError_t launch_quant_attend(const QuantAttendArgs &a, int num_sms, cudaStream_t s);
