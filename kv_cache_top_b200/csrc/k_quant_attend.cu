@@ -107,22 +107,21 @@ __device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers,
 {
     *at = Place{0u, 0u, 0u, 0u};
     if (c.bh > 32 * PER || c.bh > workers) return 0;
-    uint32_t nb[PER], total = 0;         // nb[i]: block count of pair lane + 32 i
+    uint32_t nb[PER], blocks = 0;        // of the pairs PER lane + i
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-        const int p = lane + 32 * i;
+        const int p = PER * lane + i;
         nb[i] = p < c.bh ? block_count(c, p) : 0u;
-        total += nb[i];
+        blocks += nb[i];
     }
-    total = __reduce_add_sync(kFull, total);
+    const uint32_t total = __reduce_add_sync(kFull, blocks);
     const uint32_t even = even_share(total, workers, SPAN);
     {
         const uint32_t share = even + warp;
         const float inv = __frcp_rn((float)share);
         uint32_t k = 0;                  // workers at this share
 #pragma unroll
-        for (int i = 0; i < PER; i++)
-            if (32 * i < c.bh) k += ceil_share(nb[i], share, inv);
+        for (int i = 0; i < PER; i++) k += ceil_share(nb[i], share, inv);
         k = __reduce_add_sync(kFull, k);
         if (lane == 0) fits[warp] = warp <= SPAN && k <= (uint32_t)workers;
     }
@@ -131,29 +130,37 @@ __device__ __forceinline__ uint32_t plan_pairs(const QuantCache &c, int workers,
     if (ok == 0) return 0;
     const uint32_t share = even + __ffs(ok) - 1;
     const float inv = __frcp_rn((float)share);
-    uint32_t w0 = 0, f0 = 0;             // workers and blocks of the pairs before
+    uint32_t k[PER], w = 0, f = blocks;  // sums over the lanes up to this: workers and blocks
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-        if (32 * i >= c.bh) break;
-        const uint32_t k = ceil_share(nb[i], share, inv);
-        uint32_t w = k, f = nb[i];
+        k[i] = ceil_share(nb[i], share, inv);
+        w += k[i];
+    }
+    const uint32_t own = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
-            if (lane >= o) w += x, f += y;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, w, o), y = __shfl_up_sync(kFull, f, o);
+        if (lane >= o) w += x, f += y;
+    }
+    const uint32_t here = __ballot_sync(kFull, worker < w && worker >= w - own);
+    if (here) {                          // the lane that has the worker's pair
+        w -= own;
+        f -= blocks;
+        Place x = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            if (worker >= w && worker - w < k[i]) {
+                const uint32_t start = f + (worker - w) * share;
+                x = Place{(uint32_t)(PER * lane + i), f, start, min(f + nb[i], start + share)};
+            }
+            w += k[i];
+            f += nb[i];
         }
-        const uint32_t we = w0 + w, first = f0 + f - nb[i];      // the lane's pair ends with worker we - 1
-        const uint32_t here = __ballot_sync(kFull, worker < we && worker >= we - k);
-        if (here) {
-            const int src = __ffs(here) - 1;
-            at->pair = src + 32 * i;
-            at->first = __shfl_sync(kFull, first, src);
-            at->start = at->first + (worker - __shfl_sync(kFull, we - k, src)) * share;
-            at->end = min(at->first + __shfl_sync(kFull, nb[i], src), at->start + share);
-            break;
-        }
-        w0 += __shfl_sync(kFull, w, 31);
-        f0 += __shfl_sync(kFull, f, 31);
+        const int src = __ffs(here) - 1;
+        at->pair = __shfl_sync(kFull, x.pair, src);
+        at->first = __shfl_sync(kFull, x.first, src);
+        at->start = __shfl_sync(kFull, x.start, src);
+        at->end = __shfl_sync(kFull, x.end, src);
     }
     return share;
 }
@@ -319,7 +326,6 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * SPAN) : "memory");
     };
     Place at;
-    // each row of 32 pairs that is planned costs 0.1 us
     uint32_t share = a.c.bh <= 32 ? plan_pairs<1, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at)
                                   : plan_pairs<SPAN == kQaWarps ? 4 : 8, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at);
     if (share > 0) {
