@@ -6,14 +6,14 @@
 // kernel, which knows each head's log-sum, adds the weights to acc.
 //
 // 144 bytes a key of HBM are the floor (64 pairs of 131072 keys, 4 heads: 184
-// us; the kernel takes 268, at a 1770 MHz power cap 300).  What bounds it is
+// us; the kernel takes 264, at a 1770 MHz power cap 299).  What bounds it is
 // the instructions that make matrix operands of codes and sums of digits: 717
 // warp instructions a block of 32 keys, issue slots 65% full, the integer pipe
 // 52%, fp32 44%, matrix 23%.  Hence bytes and not halves for the logits (292
 // us to 275), two fp32 operations an instruction (291 to 276), and 16 warps
 // with two blocks each in flight and not 8 or 12 with more (320 and 296).
 // Calls of few keys are bound by latency: two launches, a plan, one round of
-// blocks and a merge are 9.5 us.
+// blocks and a merge are 8 us.
 #include <cuda_fp16.h>
 
 #include "pk_launch.cuh"
