@@ -26,7 +26,6 @@ constexpr int kQaThreads = 32 * kQaWarps;
 constexpr int kQaStages = 2;             // blocks in flight per warp
 constexpr int kQaFew = 4;                // warps of a small worker
 constexpr int kQaGroups = kQaWarps / kQaFew;
-constexpr int kQaManyPairs = 129;        // pairs from which on workers are small (256 of 577 keys: 21 us for 22; 64 ragged ones: 37 for 35)
 constexpr int kQaCol = kD + 4;           // floats between the columns of a warp's sums in shared memory
 constexpr int kQmThreads = 256;          // merge kernel
 constexpr int kQmKeys = 2048;            // keys of a merge CTA's part of acc
@@ -46,11 +45,11 @@ struct QaSmem {
     float qscale[kQaGroups][2][kMaxGroup];
     uint32_t ws[kQaWarps + 1];
     float factor[kQaWarps][8];           // of a warp's column in the segment's sums
-    uint32_t fits[kQaWarps];
+    uint32_t fits[2][kQaWarps];
     Place place[kQaGroups];
     uint32_t share[kQaGroups];           // blocks a worker takes; by pairs: bit 31 (for the thread that writes it)
     int has[kQaWarps];
-    alignas(16) uint32_t q[kQaGroups][2][kMaxGroup][4][4][8];      // last: as many workers as the CTA has; [worker][segment parity][head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
+    alignas(16) uint32_t q[kQaGroups * 2 * kMaxGroup][4][4][8];  // last: as many as are used; [worker, segment parity, head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
 };
 static_assert(offsetof(QaSmem, bar) % 16 == 0 && offsetof(QaSmem, ks) % 16 == 0 && offsetof(QaSmem, vs) % 16 == 0 && offsetof(QaSmem, size) % 16 == 0 &&
               offsetof(QaSmem, q) % 16 == 0, "read 8 and 16 bytes at a time");
@@ -303,56 +302,16 @@ __device__ __forceinline__ void load_q(float v[4], const QuantAttendArgs &a, int
 // the low parts are the columns 4..7, else they are a second product.
 // The reference maximum is of logit + exponent of the key's largest value
 // scale, so that w, not p, is what stays within a half's range.
-//
-// A worker is a CTA, or (SPAN) 4 warps of one: with many pairs, small workers
-// lose less to rounds that do not fill their warps, and to merges.
-template <bool WIDE, int SPAN>
-__global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs a)
+template <bool WIDE, int SPAN, int TURNS>
+__device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &sm, const Place &at, uint32_t share)
 {
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    QaSmem &sm = *reinterpret_cast<QaSmem *>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, G = a.G;
-    if (lane < kQaStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sm.bar[warp][lane])) : "memory");
-    pdl_wait();
-    asm volatile("fence.proxy.async;" ::: "memory");     // the barriers, and rows that earlier kernels wrote
-    pdl_trigger();
-
-    // this worker's blocks [x0, end) of all, and the pair of the first
-    constexpr int kGroups = kQaWarps / SPAN;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, G = a.G;
     const int group = warp / SPAN, mate = warp % SPAN;           // worker within the CTA, warp within the worker
-    const uint32_t worker0 = blockIdx.x * kGroups, worker = worker0 + group;
+    const uint32_t worker = blockIdx.x * (kQaWarps / SPAN) + group;
     auto sync = [&]() {
         if (SPAN == kQaWarps) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * SPAN) : "memory");
     };
-    Place at;
-    uint32_t share = a.c.bh <= 32 ? plan_pairs<1, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at)
-                                  : plan_pairs<SPAN == kQaWarps ? 4 : 8, SPAN>(a.c, a.workers, worker, warp, lane, sm.fits, &at);
-    if (share > 0) {
-        share |= 0x80000000u;
-    } else {
-        const uint32_t total = count_blocks(a.c, sm.ws);
-        share = even_share(total, a.workers, SPAN);
-        if (worker0 * share >= total) return;
-        if (tid < kGroups) sm.place[tid].end = 0;        // no work unless there are blocks for it
-        for (uint32_t base = 0, c = 0;; c += kQaThreads) {
-            const uint32_t v = c + tid < (uint32_t)a.c.bh ? block_count(a.c, c + tid) : 0u;
-            uint32_t sum, last = 0;
-            const uint32_t before = base + block_excl_scan<kQaThreads>(v, sm.ws, &sum);
-#pragma unroll
-            for (int j = 0; j < kGroups; j++) {
-                const uint32_t x = (worker0 + j) * share;
-                if (x >= before && x - before < v) {
-                    sm.place[j] = Place{c + tid, before, x, min(total, x + share)};
-                }
-                if (x < total) last = x;
-            }
-            base += sum;
-            if (base > last) break;
-        }
-        __syncthreads();
-        at = sm.place[group];
-    }
     const uint32_t x0 = at.start, end = at.end;
     if (end == 0) return;
     if (mate == 0 && lane == 0) sm.share[group] = share;
@@ -385,6 +344,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
 
     constexpr int kHeads = (kMaxGroup + SPAN - 1) / SPAN;        // heads whose q a warp stages
     float qv[kHeads][4];
+    auto q_of = [&](int turn, int h) { return (group * TURNS + (TURNS > 1 ? turn : 0)) * (WIDE ? kMaxGroup : 4) + h; };
     auto bring_q = [&](int pair) {
 #pragma unroll
         for (int i = 0; i < kHeads; i++)
@@ -394,7 +354,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
 #pragma unroll
         for (int i = 0; i < kHeads; i++) {
             const int h = mate + i * SPAN;
-            if (h < G) stage_q(qv[i], a.scale2, sm.q[group][turn][h], &sm.qscale[group][turn][h], lane);
+            if (h < G) stage_q(qv[i], a.scale2, sm.q[q_of(turn, h)], &sm.qscale[group][turn][h], lane);
         }
     };
     bring_q(p);                          // ahead of the copies, which fill the memory's queues
@@ -423,7 +383,7 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
             for (int r = 0; r < 4; r++)
 #pragma unroll
                 for (int k = 0; k < (WIDE ? 3 : 2); k++) {
-                    const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[group][turn][head][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
+                    const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[q_of(turn, head)][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
                     qd[r][k < 2 ? k : 4] = head < G ? d.x : 0u;
                     qd[r][k < 2 ? k + 2 : 5] = head < G ? d.y : 0u;
                 }
@@ -639,6 +599,67 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     if (late && lane == 0 && a.c.status && atomicCAS(a.c.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.c.status[1] = p;
 }
 
+// A worker is a CTA, or 4 warps of one.  Large workers leave fewer partial
+// results; small ones lose less to rounds that do not fill their warps, and
+// there are enough of them to take one pair each where lengths differ much.
+// kFewPairs: large by pairs, else large evenly.  kSomePairs: large by pairs, else
+// small by pairs, else large evenly (96 ragged pairs of up to 9001 keys: 29 us,
+// 51 without the small; their code costs a long pair's loop registers: 64 pairs
+// of 131072 keys 265 us for 263, 8 of 1048576 314 for 303, hence not for few
+// pairs).  kManyPairs: small by pairs, else small evenly (256 pairs of 577 keys:
+// 17 us, 20 large).
+enum Workers { kFewPairs, kSomePairs, kManyPairs };
+constexpr int kQaFewPairs = 32, kQaManyPairs = 129;      // up to, and from
+template <bool WIDE, Workers KIND>
+__global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs a)
+{
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    QaSmem &sm = *reinterpret_cast<QaSmem *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lane < kQaStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sm.bar[warp][lane])) : "memory");
+    pdl_wait();
+    asm volatile("fence.proxy.async;" ::: "memory");     // the barriers, and rows that earlier kernels wrote
+    pdl_trigger();
+
+    // the worker's blocks, and the pair of the first
+    Place at;
+    uint32_t share = 0;
+    const int ctas = (int)gridDim.x;
+    bool large = KIND != kManyPairs;
+    if (large) share = plan_pairs<KIND == kFewPairs ? 1 : 4, kQaWarps>(a.c, ctas, blockIdx.x, warp, lane, sm.fits[0], &at);
+    if (KIND != kFewPairs && share == 0) {
+        const uint32_t worker = blockIdx.x * kQaGroups + warp / kQaFew;
+        share = plan_pairs<8, kQaFew>(a.c, ctas * kQaGroups, worker, warp, lane, sm.fits[1], &at);
+        if (share > 0) large = false;
+    }
+    if (share > 0) {
+        share |= 0x80000000u;
+    } else {
+        const int groups = large ? 1 : kQaGroups;
+        const uint32_t total = count_blocks(a.c, sm.ws), worker0 = blockIdx.x * groups;
+        share = even_share(total, ctas * groups, kQaWarps / groups);
+        if (worker0 * share >= total) return;
+        if (tid < groups) sm.place[tid].end = 0;         // no work unless there are blocks for it
+        for (uint32_t base = 0, c = 0;; c += kQaThreads) {
+            const uint32_t v = c + tid < (uint32_t)a.c.bh ? block_count(a.c, c + tid) : 0u;
+            uint32_t sum, last = 0;
+            const uint32_t before = base + block_excl_scan<kQaThreads>(v, sm.ws, &sum);
+            for (int j = 0; j < groups; j++) {
+                const uint32_t x = (worker0 + j) * share;
+                if (x >= before && x - before < v) sm.place[j] = Place{c + tid, before, x, min(total, x + share)};
+                if (x < total) last = x;
+            }
+            base += sum;
+            if (base > last) break;
+        }
+        __syncthreads();
+        at = sm.place[large ? 0 : warp / kQaFew];
+    }
+    if (KIND == kManyPairs) attend_blocks<WIDE, kQaFew, 2>(a, sm, at, share);
+    else if (KIND == kFewPairs || large) attend_blocks<WIDE, kQaWarps, 2>(a, sm, at, share);
+    else attend_blocks<WIDE, kQaFew, 1>(a, sm, at, share);       // one pair: no q of a next one
+}
+
 // One channel of a head's output and the head's log-sum from its ns partial
 // results at pg, N at a time, all that is needed of them in flight at once:
 // every thread sums the head's weights too, one round trip to memory instead of
@@ -771,17 +792,19 @@ __global__ void __launch_bounds__(kQmThreads, WIDE ? 3 : 4) k_quant_merge(QuantA
 
 cudaError_t launch_quant_attend(const QuantAttendArgs &args, int num_sms, cudaStream_t s)
 {
-    static std::atomic<int> done[4][kMaxDevices];
+    static std::atomic<int> done[6][kMaxDevices];
     QuantAttendArgs a = args;
-    const bool few = a.c.bh >= kQaManyPairs;
-    const int kind = (a.G > 4) + 2 * few;
-    auto kern = kind == 3 ? k_quant_attend<true, kQaFew> : kind == 2 ? k_quant_attend<false, kQaFew>
-              : kind == 1 ? k_quant_attend<true, kQaWarps> : k_quant_attend<false, kQaWarps>;
+    const bool wide = a.G > 4;
+    const Workers kind = a.c.bh <= kQaFewPairs ? kFewPairs : a.c.bh < kQaManyPairs ? kSomePairs : kManyPairs;
+    auto kern = kind == kFewPairs    ? (wide ? k_quant_attend<true, kFewPairs> : k_quant_attend<false, kFewPairs>)
+                : kind == kSomePairs ? (wide ? k_quant_attend<true, kSomePairs> : k_quant_attend<false, kSomePairs>)
+                                     : (wide ? k_quant_attend<true, kManyPairs> : k_quant_attend<false, kManyPairs>);
     const int ctas = min(num_sms, kQMaxWorkers / kQaGroups);
-    a.span = few ? kQaFew : kQaWarps;
-    a.workers = ctas * (kQaWarps / a.span);
-    cudaError_t e = dyn_smem_limit(kern, (int)sizeof(QaSmem), done[kind]);
-    const size_t smem = offsetof(QaSmem, q) + (kQaWarps / a.span) * sizeof(QaSmem::q) / kQaGroups;
+    // q of two pairs for one worker or 4, or of one for 4; no more, the rest is cache (32 KB more: 8 pairs of 32768 keys
+    // 24 us for 22)
+    const int staged = (kind == kFewPairs ? 2 : kind == kSomePairs ? 4 : 8) * (wide ? kMaxGroup : 4);
+    const size_t smem = offsetof(QaSmem, q) + staged * sizeof(QaSmem::q) / (kQaGroups * 2 * kMaxGroup);
+    cudaError_t e = dyn_smem_limit(kern, (int)smem, done[2 * kind + wide]);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kQaThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     const unsigned parts = a.accumulate ? (unsigned)((a.c.n_cap + kQmKeys - 1) / kQmKeys) : 0u;

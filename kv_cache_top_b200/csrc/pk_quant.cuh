@@ -73,7 +73,6 @@ struct QuantAttendArgs {
     uint2 *parts;            // [bh]: first worker and number of partial results of a pair that has keys
     float *logits;           // [bh][n_cap / 32][G][32] (log2 units) when accumulating, else null
     int32_t G, is_bf16, accumulate;
-    int32_t workers, span;   // workers, and warps of one
     int32_t outs;            // merge kernel: CTAs per pair that write outputs
     float scale2;            // softmax scale * log2(e)
 };
