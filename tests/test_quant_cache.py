@@ -385,7 +385,8 @@ def test_attend_lengths_from_none_to_many(pk, dtype, G):
     ("f32", 5, [0, 700, 33] * 33), ("f32", 8, [90, 0, 31, 700] * 50), ("bf16", 7, [64] * 128), ("bf16", 6, [130] * 129),
     ("bf16", 3, [33] * 256), ("f32", 8, [65] * 257),
     ("bf16", 4, [(37 * i * i + 11 * i) % 3001 for i in range(100)]), ("f32", 7, [(53 * i * i + 7 * i) % 2500 for i in range(70)]),
-    ("bf16", 5, [3000] * 60), ("f32", 2, [2100] * 100),
+    ("bf16", 5, [3000] * 60), ("f32", 2, [2100] * 100), ("f32", 7, [(37 * i * i + 11 * i) % 3001 for i in range(100)]),
+    ("bf16", 2, [5000] * 100),
 ])
 def test_attend_splits(pk, dtype, G, lens):
     """Long pairs over many workers, many pairs in one worker, nothing at all."""
