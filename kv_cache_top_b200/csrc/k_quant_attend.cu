@@ -660,41 +660,48 @@ __global__ void __launch_bounds__(kQaThreads, 1) k_quant_attend(QuantAttendArgs 
     else attend_blocks<WIDE, kQaFew, 1>(a, sm, at, share);       // one pair: no q of a next one
 }
 
-// One channel of a head's output and the head's log-sum from its ns partial
-// results at pg, N at a time, all that is needed of them in flight at once:
-// every thread sums the head's weights too, one round trip to memory instead of
-// two and a barrier (64 ragged pairs: 33 us for 35).  More than 6 at a time cost
-// more instructions than they save in latency (8 pairs of 18 partial results:
-// 24.2 us, 24.7 by 8, 25.8 by 18; 256 pairs of 2: 20.0 us, 22.5 by 8).
+// Joined partial results of a head: reference, weights' sum, one channel's sum.
+struct Joined {
+    float top, l, o;
+    __device__ float ref() const { return top == -INFINITY ? 0.0f : top; }
+    __device__ float out() const { return l == 0.0f ? 0.0f : o / l; }
+    __device__ float lse() const { return (log2f(l) + ref()) * 0.69314718055994531f; }
+};
+
+// Of the head's ns partial results at pg those first, first + step ..: N at a
+// time, all that is needed of them in flight at once.  Every thread sums the
+// head's weights too, one round trip to memory instead of two and a barrier (64
+// ragged pairs: 33 us for 35).  More than 6 at a time cost more instructions
+// than they save in latency (8 pairs of 18 partial results: 24.2 us, 24.7 by 8,
+// 25.8 by 18; 256 pairs of 2: 20.0 us, 22.5 by 8).
 template <int N>
-__device__ __forceinline__ float2 merge_parts(const float *pg, int64_t stride, int ns, int c)
+__device__ __forceinline__ Joined join_parts(const float *pg, int64_t stride, int ns, int c, int first = 0, int step = 1)
 {
-    float top = -INFINITY, l = 0.0f, o = 0.0f, ref = 0.0f;
-    for (int s = 0; s < ns; s += N) {
+    Joined j = {-INFINITY, 0.0f, 0.0f};
+    for (int s = first; s < ns; s += N * step) {
         float m[N], w[N], x[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float *q = pg + (s + i) * stride;
-            const bool in = s + i < ns;
+            const float *q = pg + (s + i * step) * stride;
+            const bool in = s + i * step < ns;
             m[i] = in ? q[kD] : -INFINITY;
             w[i] = in ? q[kD + 1] : 0.0f;
             x[i] = in ? q[c] : 0.0f;
         }
-        const float old = top;
+        const float old = j.top;
 #pragma unroll
-        for (int i = 0; i < N; i++) top = fmaxf(top, m[i]);
-        ref = top == -INFINITY ? 0.0f : top;
-        const float down = ex2(old - ref);
-        l *= down;
-        o *= down;
+        for (int i = 0; i < N; i++) j.top = fmaxf(j.top, m[i]);
+        const float ref = j.ref(), down = ex2(old - ref);
+        j.l *= down;
+        j.o *= down;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float f = ex2(m[i] - ref);
-            l = fmaf(f, w[i], l);
-            o = fmaf(f, x[i], o);
+            j.l = fmaf(f, w[i], j.l);
+            j.o = fmaf(f, x[i], j.o);
         }
     }
-    return make_float2(l == 0.0f ? 0.0f : o / l, (log2f(l) + ref) * 0.69314718055994531f);
+    return j;
 }
 
 // Merge of a pair's partial results (the first a.outs CTAs) and its part of acc
@@ -724,11 +731,32 @@ __global__ void __launch_bounds__(kQmThreads, WIDE ? 3 : 4) k_quant_merge(QuantA
     if (is_out) {
         const uint2 at = *parts;
         const int ns = (int)at.y;
+        if (a.sliced) {                  // 32 channels of a head a CTA, each warp a share of the partial results
+            constexpr int kSlices = kQmThreads / 32, kParts = kD / 32;
+            __shared__ Joined s_join[kSlices][32];
+            const int h = (int)blockIdx.x / kParts, c = (int)blockIdx.x % kParts * 32 + lane;
+            const float *pg = a.part + (int64_t)(p + at.x) * stride + h * kQPart;
+            s_join[warp][lane] = ns <= 2 * kSlices ? join_parts<2>(pg, stride, ns, c, warp, kSlices) : join_parts<4>(pg, stride, ns, c, warp, kSlices);
+            __syncthreads();
+            if (warp > 0) return;
+            Joined j = {-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kSlices; w++) j.top = fmaxf(j.top, s_join[w][lane].top);
+#pragma unroll
+            for (int w = 0; w < kSlices; w++) {
+                const float f = ex2(s_join[w][lane].top - j.ref());
+                j.l = fmaf(f, s_join[w][lane].l, j.l);
+                j.o = fmaf(f, s_join[w][lane].o, j.o);
+            }
+            a.out[((int64_t)p * G + h) * kD + c] = j.out();
+            if (c == 0 && a.lse) a.lse[(int64_t)p * G + h] = j.lse();
+            return;
+        }
         for (int e = (int)blockIdx.x * kQmThreads + tid; e < G * kD; e += outs * kQmThreads) {
             const float *pg = a.part + (int64_t)(p + at.x) * stride + e / kD * kQPart;
-            const float2 v = ns <= 2 ? merge_parts<2>(pg, stride, ns, e % kD) : merge_parts<6>(pg, stride, ns, e % kD);
-            a.out[(int64_t)p * G * kD + e] = v.x;
-            if (e % kD == 0 && a.lse) a.lse[(int64_t)p * G + e / kD] = v.y;
+            const Joined j = ns <= 2 ? join_parts<2>(pg, stride, ns, e % kD) : join_parts<6>(pg, stride, ns, e % kD);
+            a.out[(int64_t)p * G * kD + e] = j.out();
+            if (e % kD == 0 && a.lse) a.lse[(int64_t)p * G + e / kD] = j.lse();
         }
         return;
     }
@@ -808,8 +836,12 @@ cudaError_t launch_quant_attend(const QuantAttendArgs &args, int num_sms, cudaSt
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kQaThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     const unsigned parts = a.accumulate ? (unsigned)((a.c.n_cap + kQmKeys - 1) / kQmKeys) : 0u;
-    // few pairs have many partial results each: one pass a CTA; many have few: fewer CTAs (256 pairs: 22 us for 24)
-    a.outs = a.c.bh < num_sms ? (a.G + kQmHeads - 1) / kQmHeads : 1;
+    // few pairs have many partial results each: 32 channels of a head a CTA, if the CTAs are all there at once (1 pair of
+    // 131072 keys: 17 us for 27; 16 of 4096: 10.0 for 11.9; 2 of 500 8.9 for 8.5); others have fewer: one pass a CTA; many
+    // have few: fewer CTAs (256 pairs: 22 us for 24)
+    a.sliced = a.c.n_cap >= 8 * min_share(kQaWarps) * kQKeys && a.c.bh * a.G <= num_sms &&
+               a.c.bh * (a.G * (kD / 32) + (int64_t)parts) <= 4 * num_sms;
+    a.outs = a.sliced ? a.G * (kD / 32) : a.c.bh < num_sms ? (a.G + kQmHeads - 1) / kQmHeads : 1;
     return launch_pdl(a.G > 4 ? k_quant_merge<true> : k_quant_merge<false>, dim3(a.outs + parts, a.c.bh), dim3(kQmThreads), 0, s, a);
 }
 

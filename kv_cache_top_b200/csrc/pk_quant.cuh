@@ -74,6 +74,7 @@ struct QuantAttendArgs {
     float *logits;           // [bh][n_cap / 32][G][32] (log2 units) when accumulating, else null
     int32_t G, is_bf16, accumulate;
     int32_t outs;            // merge kernel: CTAs per pair that write outputs
+    int32_t sliced;          // ... of 32 channels of a head each
     float scale2;            // softmax scale * log2(e)
 };
 
