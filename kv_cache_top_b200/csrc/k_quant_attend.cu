@@ -6,7 +6,7 @@
 // kernel, which knows each head's log-sum, adds the weights to acc.
 //
 // 144 bytes a key of HBM are the floor (64 pairs of 131072 keys, 4 heads: 184
-// us; the kernel takes 264, at a 1770 MHz power cap 299).  What bounds it is
+// us; the kernel takes 266, at a 1770 MHz power cap 300).  What bounds it is
 // the instructions that make matrix operands of codes and sums of digits: 717
 // warp instructions a block of 32 keys, issue slots 65% full, the integer pipe
 // 52%, fp32 44%, matrix 23%.  Hence bytes and not halves for the logits (292
