@@ -635,7 +635,77 @@ def test_evict_crowded_weights(pk, bh, n, kind):
     assert torch.equal(dst.tensors[2][:, :budget].view(torch.int32), acc.gather(1, want).view(torch.int32))
 
 
+@gpu
+@pytest.mark.parametrize("bh,n", [(1, 131104), (3, 1048576), (20, 40000), (40, 17000), (5, 9000)])
+def test_evict_without_a_list(pk, bh, n):
+    """Neither keep nor dst's acc: the same rows as with both, with keep alone and with acc alone."""
+    cap = -(-n // KEYS) * KEYS
+    g = torch.Generator(device="cuda").manual_seed(n)
+    blocks = torch.randint(0, 256, (bh, cap // KEYS, BLOCK), generator=g, device="cuda", dtype=torch.uint8)
+    src = pk.pk_quant_view(blocks, torch.full((bh,), n, dtype=torch.int32, device="cuda"), pk.PK_BF16,
+                           acc=torch.randn(bh, cap, generator=g, device="cuda"))
+    got = []
+    for with_keep, with_acc in ((True, True), (False, False), (True, False), (False, True)):
+        dst = pk.pk_quant_view(torch.zeros(bh, 63, BLOCK, dtype=torch.uint8, device="cuda"), torch.zeros(bh, dtype=torch.int32, device="cuda"),
+                               pk.PK_BF16, acc=torch.zeros(bh, 63 * KEYS, device="cuda") if with_acc else None)
+        keep = torch.zeros(bh, 2001, dtype=torch.int32, device="cuda") if with_keep else None
+        pk.pk_quant_evict(src, dst, 2001, sink=9, recent=100, keep=keep)
+        assert dst.tensors[1].tolist() == [2001] * bh
+        got.append(dst.tensors[0])
+    assert all(torch.equal(got[0], x) for x in got[1:])
+
+
 # ---------------------------------------------------------------- together
+@gpu
+@pytest.mark.parametrize("G", [1, 5])
+def test_rows_beyond_4_gigabytes(pk, G):
+    """Pairs of 16 million keys, 7 GB: rows at their ends are written, attended, evicted and read back."""
+    bh, n_cap, m = 3, (1 << 24) + 64, 40
+    rng = np.random.default_rng(16)
+    blocks = torch.zeros(bh, n_cap // KEYS, BLOCK, dtype=torch.uint8, device="cuda")      # scales of zero: keys and values of zero
+    lens = torch.zeros(bh, dtype=torch.int32, device="cuda")
+    c = pk.pk_quant_view(blocks, lens, pk.PK_F32, acc=torch.zeros(bh, n_cap, device="cuda"), status=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    K, V = make_rows(rng, bh * m, torch.float32).view(bh, m, D), make_rows(rng, bh * m, torch.float32).view(bh, m, D)
+    at = torch.tensor([n_cap - m, n_cap - m - 7, n_cap - 2 * m], dtype=torch.int32, device="cuda")
+    pk.pk_quant_append(c, K.cuda(), V.cuda(), m, at=at)
+    n = [int(x) for x in lens.tolist()]
+    assert n == [a + m for a in at.tolist()]
+    Kq, Vq = (torch.from_numpy(np.stack([ref.stored(x[p].numpy())[2] for p in range(bh)])) for x in (K, V))
+    k, v = torch.zeros(bh, m, D, device="cuda"), torch.zeros(bh, m, D, device="cuda")
+    pk.pk_quant_rows(c, m, k, v, at=at)
+    assert torch.equal(k.cpu().double(), Kq.float().double()) and torch.equal(v.cpu().double(), Vq.float().double())
+    # logits of about 25 at the end against 16 million of zero
+    q = torch.stack([K[:, (7 * g + 3) % m] for g in range(G)], 1)
+    q = (q * (25 * math.sqrt(D) / (q * q).sum(-1, keepdim=True))).float()
+    out, lse = torch.zeros(bh, G, D, device="cuda"), torch.zeros(bh, G, device="cuda")
+    work = torch.empty(pk.pk_quant_attend_workspace(c, G, True), dtype=torch.uint8, device="cuda")
+    pk.pk_quant_attend(c, q.cuda(), G, out, work, lse=lse, accumulate=True)
+    acc = c.tensors[2]
+    for p in range(bh):
+        z = q[p].double() @ Kq[p].double().T / math.sqrt(D)
+        total = torch.exp(z).sum(1) + (n[p] - m)
+        w = torch.exp(z) / total[:, None]
+        # fp32 logits up to 25 (1e-6 relative each: 3e-5 of a weight, 1e-5 of a product at most), sums of 2^24 terms
+        assert torch.allclose(out[p].cpu().double(), w @ Vq[p].double(), rtol=0, atol=2e-4 * float(Vq.abs().max()))
+        assert torch.allclose(lse[p].cpu().double(), torch.log(total), rtol=0, atol=2e-4)
+        assert torch.allclose(acc[p, n[p] - m:n[p]].cpu().double(), w.sum(0), rtol=2e-4, atol=0)
+        assert torch.allclose(acc[p, :n[p] - m].double().sum().cpu(), ((n[p] - m) / total).sum(), rtol=2e-4)
+        assert acc[p, n[p]:].abs().max() == 0 if n[p] < n_cap else True
+    e = pk.pk_quant_view(torch.zeros(bh, 2, BLOCK, dtype=torch.uint8, device="cuda"), torch.zeros(bh, dtype=torch.int32, device="cuda"), pk.PK_F32)
+    keep = torch.zeros(bh, m, dtype=torch.int32, device="cuda")
+    pk.pk_quant_evict(c, e, m, recent=m // 2, keep=keep)
+    pk.pk_quant_rows(e, m, k, v)
+    for p in range(bh):
+        order = torch.sort(acc[p, :n[p] - m // 2], descending=True, stable=True).indices[:m - m // 2].sort().values
+        want = torch.cat([order, torch.arange(n[p] - m // 2, n[p], device="cuda")])
+        assert torch.equal(keep[p].long(), want)
+        for i, slot in enumerate(want.tolist()):
+            j = slot - (n[p] - m)
+            assert torch.equal(k[p, i].cpu(), Kq[p, j].float() if j >= 0 else torch.zeros(D))
+            assert torch.equal(v[p, i].cpu(), Vq[p, j].float() if j >= 0 else torch.zeros(D))
+    assert c.tensors[3].tolist() == [0, 0]
+
+
 @gpu
 def test_first_calls_may_be_captured(pk):
     """A process whose first calls are recorded into a graph."""
