@@ -43,7 +43,7 @@ struct QeSmem {
     uint32_t hist[kQeBins];
     uint8_t marks[kQeTile / 4];          // of 4 slots: bits 0..3 those that stay, 4..7 those that tie
     uint32_t ws[kQeThreads / 32 + 1];
-    uint32_t digit, left;
+    uint32_t digit, left, whole;
     unsigned long long bar;              // bulk copies of the weights
 };
 static_assert(kQeTile == 32 * kQeThreads, "a thread has one group of the slots");
@@ -57,7 +57,7 @@ constexpr int kQsMany = 256, kQsFew = 1024;
 template <int NT>
 struct QsState {
     uint32_t ws[NT / 32 + 1];
-    uint32_t digit, left;
+    uint32_t digit, left, whole;
     uint32_t count[2];                   // kept and tied slots of this CTA
     uint32_t all[kQeMaxCluster];         // `cands` of the cluster's CTAs
     uint32_t ahead[2];                   // of the CTAs before: slots put aside that stay, and that tie
@@ -110,10 +110,12 @@ __device__ __forceinline__ uint32_t weight_key(float x)
 // The weight of a key (not NaN's).
 __device__ __forceinline__ float key_weight(uint32_t k) { return unord_f32(k); }
 
-// The bin of the left-th largest key by the counts `sums`: *digit, and in *left
-// its rank within the bin; over a CTA of NT threads.
+// The bin of the left-th largest key by the counts `sums`: *digit, in *rank its
+// rank within the bin, and in *whole whether that is the bin's last; over a CTA
+// of NT threads.
 template <int NT>
-__device__ __forceinline__ void find_digit(const uint32_t *sums, int bins, uint32_t *ws, uint32_t left, uint32_t *digit, uint32_t *rank)
+__device__ __forceinline__ void find_digit(const uint32_t *sums, int bins, uint32_t *ws, uint32_t left, uint32_t *digit, uint32_t *rank,
+                                           uint32_t *whole)
 {
     constexpr int kMost = kQeBins / NT;
     const int per = bins / NT, tid = threadIdx.x;
@@ -130,11 +132,17 @@ __device__ __forceinline__ void find_digit(const uint32_t *sums, int bins, uint3
         if (over < left && over + mine[e] >= left) {
             *digit = per * tid + e;
             *rank = left - over;
+            *whole = left - over == mine[e];
         }
         over += mine[e];
     }
     __syncthreads();
 }
+
+// After the second digit: where the whole bin stays the third is not needed, the
+// threshold is just below the bin and nothing ties (64 pairs of 1600 keys: 21.7
+// us for 22.5).  Not next to zero, whose two signs are one weight.
+__device__ __forceinline__ bool bin_stays(uint32_t whole, uint32_t prefix) { return whole && prefix > 0x80000000u; }
 
 // Up to 32 rows to slots o .. o + m - 1 of dst by a warp, lane j < m with the
 // source slot of row j: 16 bytes a lane, all loads in flight.
@@ -283,10 +291,16 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
                         atomicAdd(&sm.hist[(k[e] >> g.shift) & (g.bins - 1)], 1u);
             }
             __syncthreads();
-            find_digit<kQeThreads>(sm.hist, g.bins, sm.ws, left, &sm.digit, &sm.left);
+            find_digit<kQeThreads>(sm.hist, g.bins, sm.ws, left, &sm.digit, &sm.left, &sm.whole);
             prefix |= sm.digit << g.shift;
             left = sm.left;
+            const bool stays = d == 1 && bin_stays(sm.whole, prefix);
             __syncthreads();
+            if (stays) {
+                prefix--;
+                left = 0;
+                break;
+            }
         }
     }
     for (int i = 4 * tid; i < n; i += 4 * kQeThreads) {
@@ -497,10 +511,16 @@ __device__ __forceinline__ void quant_select(const QuantEvictArgs &a, QsSmem<NT>
                         if ((k & h.above) == prefix) atomicAdd(&sm.sums[(k >> h.shift) & (h.bins - 1)], 1u);
                     });
                     __syncthreads();
-                    find_digit<NT>(sm.sums, h.bins, sm.ws, left, &sm.digit, &sm.left);
+                    find_digit<NT>(sm.sums, h.bins, sm.ws, left, &sm.digit, &sm.left, &sm.whole);
                     prefix |= sm.digit << h.shift;
                     left = sm.left;
+                    const bool stays = e == 1 && bin_stays(sm.whole, prefix);
                     __syncthreads();
+                    if (stays) {
+                        prefix--;
+                        left = 0;
+                        break;
+                    }
                 }
                 break;
             }
@@ -517,15 +537,21 @@ __device__ __forceinline__ void quant_select(const QuantEvictArgs &a, QsSmem<NT>
                     if (w < ranks) cluster.map_shared_rank(sm.sums, w)[rank * share + i] = v;
             }
             cluster.sync();
-            find_digit<NT>(sm.sums, g.bins, sm.ws, left, &sm.digit, &sm.left);
+            find_digit<NT>(sm.sums, g.bins, sm.ws, left, &sm.digit, &sm.left, &sm.whole);
             const uint32_t digit = sm.digit;
             prefix |= digit << g.shift;
             left = sm.left;
+            const bool stays = d == 1 && bin_stays(sm.whole, prefix);
             for (int i = tid; i < g.bins; i += NT)
-                if (i > (int)digit) own += sm.hist[0][i];
+                if (i + (int)stays > (int)digit) own += sm.hist[0][i];
             if (d == 2) ties = sm.hist[0][digit];
             if (d == 1) marks_done = once && sm.cands <= Smem::kCands;
             __syncthreads();
+            if (stays) {
+                prefix--;
+                left = 0;
+                break;
+            }
         }
         if (marks_done)                  // the other slots that stay or tie
             for (int i = tid; i < (int)sm.cands; i += NT) {

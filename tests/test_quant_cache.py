@@ -636,6 +636,34 @@ def test_evict_crowded_weights(pk, bh, n, kind):
 
 
 @gpu
+@pytest.mark.parametrize("bh,n", [(3, 200), (3, 9000), (20, 40000), (2, 131104), (2, 2200000)])
+@pytest.mark.parametrize("low,high,rest", [
+    (0x3f800800, 0x3f800fff, 0x3f8007ff), (0x3f800800, 0x3f800fff, 0x3f000000), (0x00000000, 0x000007ff, 0x80000001),
+    (0x00000800, 0x00000fff, 0x000007ff), (0x00000000, 0x00000000, 0x80000000), (0x80000000, 0x80000000, 0x80000800),
+    (0xff800000, 0xff800000, 0x7fc00000), (0x7f800000, 0x7f800000, 0x7f7fffff), (0x007fffff, 0x00800000, 0x00000001),
+])
+def test_evict_threshold_at_the_border_of_a_digit(pk, bh, n, low, high, rest):
+    """The kept weights are all those that share their first digits, or one less; the others lie right below."""
+    count = 60
+    cap = -(-n // KEYS) * KEYS
+    g = torch.Generator(device="cuda").manual_seed(n)
+    bits = torch.full((bh, cap), rest, dtype=torch.int64, device="cuda")
+    for p in range(bh):
+        at = torch.randperm(n, generator=g, device="cuda")[:count]
+        bits[p, at] = torch.randint(low, high + 1, (count,), generator=g, device="cuda")
+        bits[p, at[0]] = low
+    acc = torch.where(bits > 0x7fffffff, bits - (1 << 32), bits).to(torch.int32).view(torch.float32)
+    for budget in (count, count - 1, count + 1):
+        src = pk.pk_quant_view(torch.zeros(bh, cap // KEYS, BLOCK, dtype=torch.uint8, device="cuda"),
+                               torch.full((bh,), n, dtype=torch.int32, device="cuda"), pk.PK_F32, acc=acc)
+        dst = pk.pk_quant_view(torch.zeros(bh, 2, BLOCK, dtype=torch.uint8, device="cuda"), torch.zeros(bh, dtype=torch.int32, device="cuda"), pk.PK_F32)
+        keep = torch.zeros(bh, budget, dtype=torch.int32, device="cuda")
+        pk.pk_quant_evict(src, dst, budget, keep=keep)
+        for p in range(bh):
+            assert keep[p].tolist() == ref.evict(acc[p, :n].cpu().numpy(), n, budget, 0, 0).tolist()
+
+
+@gpu
 @pytest.mark.parametrize("bh,n", [(1, 131104), (3, 1048576), (20, 40000), (40, 17000), (5, 9000)])
 def test_evict_without_a_list(pk, bh, n):
     """Neither keep nor dst's acc: the same rows as with both, with keep alone and with acc alone."""
