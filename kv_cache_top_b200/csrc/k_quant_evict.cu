@@ -110,6 +110,15 @@ __device__ __forceinline__ uint32_t weight_key(float x)
 // The weight of a key (not NaN's).
 __device__ __forceinline__ float key_weight(uint32_t k) { return unord_f32(k); }
 
+// The largest weight whose key agrees with `prefix` in the bits `above`.  No
+// weight has the key of -0, 0x7fffffff: as a float it would take in the zeros,
+// which belong to the next digit.
+__device__ __forceinline__ float top_weight(uint32_t prefix, uint32_t above)
+{
+    const uint32_t k = prefix | ~above;
+    return key_weight(k == 0x7fffffffu ? k - 1 : min(k, 0xff800000u));       // up to infinity
+}
+
 // The bin of the left-th largest key by the counts `sums`: *digit, in *rank its
 // rank within the bin, and in *whole whether that is the bin's last; over a CTA
 // of NT threads.
@@ -421,7 +430,7 @@ __device__ __forceinline__ void quant_select(const QuantEvictArgs &a, QsSmem<NT>
             // keys that agree with the digits before are a range of weights (the first digit 0: NaN alone)
             const bool nan = d > 0 && (prefix >> 21) == 0;
             const float low = d == 0 || nan ? 0.0f : key_weight(max(prefix, 0x007fffffu));                 // -inf
-            const float high = d == 0 || nan ? 0.0f : key_weight(min(prefix | ~g.above, 0xff800000u));      // inf
+            const float high = d == 0 || nan ? 0.0f : top_weight(prefix, g.above);
             uint32_t *hist = sm.hist[d == 0 ? lane & (kQsCopies - 1) : 0];
             auto count = [&](const float x[4], int i) {
                 if (d > 0 && !nan) {                 // few
