@@ -376,7 +376,10 @@ pk_status pk_quant_attend_workspace(const pk_quant_cache *cache, int32_t group, 
 
 /* Exact softmax attention of every query head over all keys of its pair.
  *   q      [bh][group][D] kv_dtype (= [batch][H*G][D]: query head j of a
- *          sequence belongs to KV head j/G); 1 <= group <= 8.
+ *          sequence belongs to KV head j/G); 1 <= group <= 8.  Logits are
+ *          computed from q in fixed point: every channel within 2^-30 of the
+ *          largest magnitude in its group of 32 channels (of 2^-97 if all are
+ *          smaller), from there on to about fp32.
  *   scale  softmax scale; 0 = 1/sqrt(D).
  *   out    [bh][group][D] f32: sum_j p_j V_j, p = softmax_j(scale <q, K_j>);
  *          zeros for a pair without keys.

@@ -42,7 +42,7 @@ struct QaSmem {
     float4 vs[kQaWarps][kQKeys];         // ... and V
     float size[kQaWarps][kQKeys];        // exponent of each key's largest V scale
     float m[kQaWarps][8], l[kQaWarps][8];
-    float qscale[kQaGroups][2][kMaxGroup];
+    float4 qscale[kQaGroups][2][kMaxGroup];      // unit of a logit's part, by groups of channels
     uint32_t ws[kQaWarps + 1];
     float factor[kQaWarps][8];           // of a warp's column in the segment's sums
     uint32_t fits[2][kQaWarps];
@@ -52,7 +52,7 @@ struct QaSmem {
     alignas(16) uint32_t q[kQaGroups * 2 * kMaxGroup][4][4][8];  // last: as many as are used; [worker, segment parity, head][digit][group][2 t + h]: bytes of channels 32r + 8t + h + {0, 2, 4, 6}
 };
 static_assert(offsetof(QaSmem, bar) % 16 == 0 && offsetof(QaSmem, ks) % 16 == 0 && offsetof(QaSmem, vs) % 16 == 0 && offsetof(QaSmem, size) % 16 == 0 &&
-              offsetof(QaSmem, q) % 16 == 0, "read 8 and 16 bytes at a time");
+              offsetof(QaSmem, qscale) % 16 == 0 && offsetof(QaSmem, q) % 16 == 0, "read 8 and 16 bytes at a time");
 static_assert(8 * kQaCol * 4 <= kQBlock, "a warp's sums fit the block that it has consumed");
 
 // blocks a worker of `span` warps takes at least
@@ -252,19 +252,25 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return fma_half2(w & 
 constexpr float kQaLag = 1.0f;
 constexpr float kQaLift = 13.0f;
 
-// q of one head as 32-bit fixed point of its largest magnitude, in signed
-// bytes, by one warp: lane l has channels 4l .. 4l + 3.
-__device__ __forceinline__ void stage_q(const float v[4], float scale2, uint32_t (*q)[4][8], float *qscale, int lane)
+// q of one head as fixed point, in four signed bytes, of each group's largest
+// magnitude: off by at most 2^-30 of that, and exact for a bf16 that is not below
+// its 2^-22th part.  (One unit for all 128 channels would lose small ones beside a
+// large one that the keys do not have, three bytes those of the same group: with
+// one channel 1024 times the others the outputs were off by 3e-4.)  By one warp:
+// lane l has channels 4l .. 4l + 3, 8 lanes a group.
+__device__ __forceinline__ void stage_q(const float v[4], float scale2, uint32_t (*q)[4][8], float4 *qscale, int lane)
 {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    top = __reduce_max_sync(kFull, top);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
     // q 2^(156 - e) is below 2^30; a product is 16 (code - 8) times a digit of weight 2^24.  A query with an infinity
     // or NaN has NaN logits
     const uint32_t e = min(max(top >> 23, 30u), 254u);
     const float up = __uint_as_float((283u - e) << 23);
-    if (lane == 0) *qscale = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : scale2 * __uint_as_float((e - 9u) << 23);
+    if ((lane & 7) == 0)
+        reinterpret_cast<float *>(qscale)[lane >> 3] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : scale2 * __uint_as_float((e - 9u) << 23);
     uint32_t d[4];
 #pragma unroll
     for (int i = 0; i < 4; i++)          // bytes 3, 2, 1, 0: digits 0, 1, 2, 3
@@ -338,9 +344,13 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
     const int head = WIDE ? g : (g & 3);
     const float low = !WIDE && g >= 4 ? -1.0f : 0.0f;   // this column holds the weights' low parts
 
-    // x = high_digit d[0] + low_digit d[1] (+ 2^-16 d'[0]) without the sums' 1.5 2^23: every step but the last is exact
+    // high_digit d[0] + low_digit d[1] without the sums' 1.5 2^23.  Sums are multiples of 16 below 2^20, so WIDE's are exact
+    // and are joined with one rounding; else this is the rounding
     const float high_digit = WIDE || g < 4 ? 1.0f : 0x1p-8f, low_digit = WIDE ? 0x1p-8f : high_digit * 0x1p-16f;
-    const float start = -12582912.0f * (high_digit + low_digit + (WIDE ? 0x1p-16f : 0.0f));
+    const float start = -12582912.0f * (high_digit + low_digit);
+    auto joined = [&](const float2 d[2]) {
+        return fma2(d[1], make_float2(low_digit, low_digit), fma2(d[0], make_float2(high_digit, high_digit), make_float2(start, start)));
+    };
 
     constexpr int kHeads = (kMaxGroup + SPAN - 1) / SPAN;        // heads whose q a warp stages
     float qv[kHeads][4];
@@ -376,16 +386,16 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
         float2 l2 = make_float2(0.0f, 0.0f);
         int free_slot = -1;
         if (has) {
-            // a product's rows g and g + 8 hold q's digits 0 and 1, and 2 (WIDE), or g / 4 and g / 4 + 2
-            uint32_t qd[4][WIDE ? 6 : 4];
-            const float qscale = head < G ? sm.qscale[group][turn][head] : 0.0f;
+            // a product's rows g and g + 8 hold q's digits 0 and 1, and 2 and 3 (WIDE), or g / 4 and g / 4 + 2
+            uint32_t qd[4][WIDE ? 8 : 4];
+            const float4 qscale = head < G ? sm.qscale[group][turn][head] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int r = 0; r < 4; r++)
 #pragma unroll
-                for (int k = 0; k < (WIDE ? 3 : 2); k++) {
+                for (int k = 0; k < (WIDE ? 4 : 2); k++) {
                     const uint2 d = *reinterpret_cast<const uint2 *>(&sm.q[q_of(turn, head)][WIDE ? k : (g >> 2) + 2 * k][r][2 * t]);
-                    qd[r][k < 2 ? k : 4] = head < G ? d.x : 0u;
-                    qd[r][k < 2 ? k + 2 : 5] = head < G ? d.y : 0u;
+                    qd[r][2 * (k & 2) + (k & 1)] = head < G ? d.x : 0u;
+                    qd[r][2 * (k & 2) + (k & 1) + 2] = head < G ? d.y : 0u;
                 }
 #pragma unroll
             for (int r = 0; r < 4; r++)
@@ -426,17 +436,18 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
                         const uint32_t b0 = ((w << 4) & 0xf0f0f0f0u) ^ 0x80808080u, b1 = (w & 0xf0f0f0f0u) ^ 0x80808080u;   // 16 (code - 8)
                         float2 d[2], x;
                         imma16832(d, qd[r][0], qd[r][1], qd[r][2], qd[r][3], b0, b1);
-                        x = fma2(d[1], make_float2(low_digit, low_digit), fma2(d[0], make_float2(high_digit, high_digit), make_float2(start, start)));
+                        x = joined(d);
                         if (WIDE) {
-                            imma16832(d, qd[r][4], 0u, qd[r][5], 0u, b0, b1);
-                            x = fma2(d[0], make_float2(0x1p-16f, 0x1p-16f), x);
+                            imma16832(d, qd[r][4], qd[r][5], qd[r][6], qd[r][7], b0, b1);
+                            x = fma2(joined(d), make_float2(0x1p-16f, 0x1p-16f), x);
                         }
                         const float2 sc = r == 0 ? make_float2(s01.x, s01.y) : r == 1 ? make_float2(s01.z, s01.w)
                                         : r == 2 ? make_float2(s23.x, s23.y) : make_float2(s23.z, s23.w);
-                        z[i] = r ? fma2(x, sc, z[i]) : mul2(x, sc);
+                        const float f = r == 0 ? qscale.x : r == 1 ? qscale.y : r == 2 ? qscale.z : qscale.w;
+                        const float2 unit = mul2(sc, make_float2(f, f));
+                        z[i] = r ? fma2(x, unit, z[i]) : mul2(x, unit);
                     }
                     if (!WIDE) z[i] = add2(z[i], make_float2(__shfl_xor_sync(kFull, z[i].x, 16), __shfl_xor_sync(kFull, z[i].y, 16)));
-                    z[i] = mul2(z[i], make_float2(qscale, qscale));
                 }
                 if (a.logits && g < G) {
                     float *zo = a.logits + ((p * pair_blocks + b) * G + g) * kQKeys + 2 * t;

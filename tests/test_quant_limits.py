@@ -6,11 +6,112 @@ import numpy as np
 import pytest
 import torch
 
+from tests import quant_bound as bound
 from tests import quant_ref as ref
 from tests.test_quant_cache import make_cache, make_rows, pk  # noqa: F401
 
 gpu = pytest.mark.gpu
 D, KEYS, BLOCK = 128, 32, 4608
+
+
+# ---------------------------------------------------------------- accuracy of the attention
+def uneven(rng, G, n, td, ratio, where):
+    """A query whose channel 5 of 128 is `ratio` times the others; in the keys that channel is nothing ("zero"), its
+    group is ("group"), or its group is `ratio` times smaller than the others ("small")."""
+    q = make_rows(rng, G, torch.float32).numpy()
+    K, V = make_rows(rng, n, torch.float32).numpy(), make_rows(rng, n, torch.float32).numpy()
+    q[:, 5] = np.abs(q).max() * ratio
+    if where == "zero":
+        K[:, 5] = 0
+    elif where == "group":
+        K[:, :32] = 0
+    else:
+        K[:, :32] /= ratio
+    return torch.from_numpy(q).to(td), K, V
+
+
+def check_close(pk, q, kinds, rows, accumulate=True, scale=None):  # noqa: F811
+    """pk_quant_attend of q [bh][G][128] over pairs of rows (K, V) against 64 bits, within the bound of its arithmetic."""
+    bh, G = q.shape[:2]
+    lens = [len(K) for K, _ in rows]
+    cap = max(KEYS, -(-max(lens) // KEYS) * KEYS)
+    blocks = np.full((bh, cap // KEYS, BLOCK), 0xff, np.uint8)
+    for p, (K, V) in enumerate(rows):
+        if lens[p]:
+            b = ref.pack(K, V)
+            blocks[p, :len(b)] = b
+    c = pk.pk_quant_view(torch.from_numpy(blocks).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), kinds,
+                         acc=torch.zeros(bh, cap, device="cuda"))
+    out, lse = torch.zeros(bh, G, D, device="cuda"), torch.zeros(bh, G, device="cuda")
+    work = torch.empty(pk.pk_quant_attend_workspace(c, G, accumulate), dtype=torch.uint8, device="cuda")
+    pk.pk_quant_attend(c, q.cuda(), G, out, work, lse=lse, accumulate=accumulate, scale=scale or 0.0)
+    out, lse, acc = (t.cpu().double().numpy() for t in (out, lse, c.tensors[2]))
+    for p, n in enumerate(lens):
+        if n == 0:
+            assert np.all(out[p] == 0) and np.all(lse[p] == -np.inf)
+            continue
+        K, V = (x[:n] for x in ref.values(blocks[p]))
+        o, l, w, eo, el, ew = bound.attend(q[p].double().numpy(), K, V, scale)
+        assert np.all(np.abs(out[p] - o) <= eo), (p, n, np.max(np.abs(out[p] - o) / eo))
+        assert np.all(np.abs(lse[p] - l) <= el), (p, n, np.max(np.abs(lse[p] - l) / el))
+        if accumulate:                   # each weight's own error, a rounding a head
+            tol = (w * ew).sum(0) + (G + 1) * bound.U * w.sum(0) + 1e-37
+            assert np.all(np.abs(acc[p, :n] - w.sum(0)) <= tol), (p, n, np.max(np.abs(acc[p, :n] - w.sum(0)) / tol))
+
+
+@pytest.mark.parametrize("n", [2, 5, 33, 577])
+@pytest.mark.parametrize("form", ["q 15 bits", "weights as halves", "logits as halves"])
+def test_bound_tells_coarser_forms(n, form):
+    """What fewer bits would do is outside of the bound, and q as it is held well inside.  (From two keys on: a single
+    key's weight is 1, and 1 times a scale of 8 bits is a half.)"""
+    rng = np.random.default_rng(n)
+    q = (1.5 * make_rows(rng, 8, torch.float32)).double().numpy()
+    K, V = (ref.stored(make_rows(rng, n, torch.float32).numpy())[2] for _ in range(2))
+    o, l, _, eo, el, _ = bound.attend(q, K, V)
+    go, gl = bound.coarse(q, K, V, form)
+    assert np.any(np.abs(go - o) > eo) or np.any(np.abs(gl - l) > el)
+    fo, fl = bound.coarse(bound.fixed_point(q), K, V, "")
+    assert np.all(np.abs(fo - o) <= 0.5 * eo) and np.all(np.abs(fl - l) <= 0.5 * el)
+
+
+@pytest.mark.parametrize("form,where,ratio", [
+    ("q 22 bits of all", "zero", 1024), ("q 22 bits of all", "small", 1024), ("q 22 bits of all", "group", 256),
+    ("q 30 bits of all", "group", 2 ** 18), ("q 30 bits of all", "small", 2 ** 18),
+])
+def test_bound_tells_a_unit_for_all_channels(form, where, ratio):
+    """A unit for the head's largest channel, beside small ones that decide."""
+    rng = np.random.default_rng(ratio)
+    q, K, V = uneven(rng, 4, 200, torch.float32, ratio, where)
+    q = q.double().numpy()
+    K, V = ref.stored(K)[2], ref.stored(V)[2]
+    o, l, _, eo, el, _ = bound.attend(q, K, V)
+    go, gl = bound.coarse(q, K, V, form)
+    assert np.any(np.abs(go - o) > eo) and np.any(np.abs(gl - l) > el)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 4, 5, 8])
+@pytest.mark.parametrize("where", ["zero", "group", "small"])
+def test_attend_query_of_uneven_channels(pk, G, dtype, where):  # noqa: F811
+    """A channel of q far above the others that the keys hardly have: the others decide, as accurately as ever."""
+    td, kind = (torch.bfloat16, pk.PK_BF16) if dtype == "bf16" else (torch.float32, pk.PK_F32)
+    rng = np.random.default_rng(G)
+    parts = [uneven(rng, G, n, td, ratio, where) for n in (1, 33, 500) for ratio in (16, 256, 1024, 16384, 2 ** 20)]
+    check_close(pk, torch.stack([x[0] for x in parts]), kind, [x[1:] for x in parts])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 3, 4, 5, 8])
+@pytest.mark.parametrize("lens", [[1, 2, 3, 31, 32, 33, 0, 64, 100, 577], [1000, 9001], [20011], [65] * 140, [33, 700] * 20])
+def test_attend_within_the_bound_of_its_arithmetic(pk, G, dtype, lens):  # noqa: F811
+    td, kind = (torch.bfloat16, pk.PK_BF16) if dtype == "bf16" else (torch.float32, pk.PK_F32)
+    rng = np.random.default_rng(len(lens) + G)
+    q = torch.stack([(1.5 * make_rows(rng, G, torch.float32)).to(td) for _ in lens])
+    rows = [tuple(make_rows(rng, n, td).float().numpy() for _ in range(2)) for n in lens]
+    check_close(pk, q, kind, rows)
+    check_close(pk, q, kind, rows, accumulate=False, scale=0.011)
 
 
 # ---------------------------------------------------------------- eviction
