@@ -380,9 +380,11 @@ pk_status pk_quant_attend_workspace(const pk_quant_cache *cache, int32_t group, 
  *          computed from q in fixed point: every channel within 2^-30 of the
  *          largest magnitude in its group of 32 channels (of 2^-97 if all are
  *          smaller), from there on to about fp32.
- *   scale  softmax scale; 0 = 1/sqrt(D).
+ *   scale  softmax scale; 0 = 1/sqrt(D).  |scale <q, K_j>| stays below 2^23.
  *   out    [bh][group][D] f32: sum_j p_j V_j, p = softmax_j(scale <q, K_j>);
  *          zeros for a pair without keys.
+ *          For |V| up to 2^96: beside larger values weights below 2^-45 of the
+ *          largest leave fp32's range.
  *   lse    [bh][group] f32 or NULL: log sum_j exp(scale <q, K_j>) (-inf without
  *          keys): what merging with attention over other rows needs.
  *   accumulate  non-zero: acc[bh][j] += sum over the pair's query heads of p_j

@@ -222,6 +222,16 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// l 2^d where a factor 2^d may be below fp32's range.  References lie as far
+// apart as the sizes of values (2^-80 for rows of zeros, see attend_blocks); a
+// sum of values that drops out with the factor is too small to matter, the
+// weights of such rows are not.
+__device__ __forceinline__ float shifted(float l, float d)
+{
+    const float a = fmaxf(d, -100.0f);
+    return l * ex2(a) * ex2(d - a);      // the second is 1 for most
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float2 a)
 {
     const __half2 h = __floats2half2_rn(a.x, a.y);
@@ -471,9 +481,9 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
                 top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
                 if (__any_sync(kFull, top > m + kQaLag)) {     // rare: raise the reference maximum
                     const float to = top > m + kQaLag ? top : m;
-                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+                    const float d = to == -INFINITY ? 0.0f : m - to, f = ex2(d);
                     m = to;
-                    l2 = mul2(l2, make_float2(f, f));
+                    l2 = make_float2(shifted(l2.x, d), shifted(l2.y, d));
                     const float2 fc = make_float2(__shfl_sync(kFull, f, 8 * t), __shfl_sync(kFull, f, 8 * t + 4));
 #pragma unroll
                     for (int r = 0; r < 4; r++)
@@ -576,8 +586,8 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
             float top = mw;
 #pragma unroll
             for (int i = SPAN / 2; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
-            const float f = in ? ex2(mw - (top == -INFINITY ? 0.0f : top)) : 0.0f;
-            float l = in ? f * sm.l[w][h] : 0.0f;
+            const float d = mw - (top == -INFINITY ? 0.0f : top), f = in ? ex2(d) : 0.0f;
+            float l = in ? shifted(sm.l[w][h], d) : 0.0f;
 #pragma unroll
             for (int i = SPAN / 2; i; i >>= 1) l += __shfl_xor_sync(kFull, l, i);
             if (lane < SPAN) sm.factor[w][h] = f;
@@ -702,14 +712,13 @@ __device__ __forceinline__ Joined join_parts(const float *pg, int64_t stride, in
         const float old = j.top;
 #pragma unroll
         for (int i = 0; i < N; i++) j.top = fmaxf(j.top, m[i]);
-        const float ref = j.ref(), down = ex2(old - ref);
-        j.l *= down;
-        j.o *= down;
+        const float ref = j.ref();
+        j.l = shifted(j.l, old - ref);
+        j.o *= ex2(old - ref);
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float f = ex2(m[i] - ref);
-            j.l = fmaf(f, w[i], j.l);
-            j.o = fmaf(f, x[i], j.o);
+            j.l += shifted(w[i], m[i] - ref);
+            j.o = fmaf(ex2(m[i] - ref), x[i], j.o);
         }
     }
     return j;
@@ -755,9 +764,9 @@ __global__ void __launch_bounds__(kQmThreads, WIDE ? 3 : 4) k_quant_merge(QuantA
             for (int w = 0; w < kSlices; w++) j.top = fmaxf(j.top, s_join[w][lane].top);
 #pragma unroll
             for (int w = 0; w < kSlices; w++) {
-                const float f = ex2(s_join[w][lane].top - j.ref());
-                j.l = fmaf(f, s_join[w][lane].l, j.l);
-                j.o = fmaf(f, s_join[w][lane].o, j.o);
+                const float d = s_join[w][lane].top - j.ref();
+                j.l += shifted(s_join[w][lane].l, d);
+                j.o = fmaf(ex2(d), s_join[w][lane].o, j.o);
             }
             a.out[((int64_t)p * G + h) * kD + c] = j.out();
             if (c == 0 && a.lse) a.lse[(int64_t)p * G + h] = j.lse();
@@ -815,7 +824,7 @@ __global__ void __launch_bounds__(kQmThreads, WIDE ? 3 : 4) k_quant_merge(QuantA
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
         const float ref = m == -INFINITY ? 0.0f : m;
         float l = 0.0f;
-        for (int s = lane; s < ns; s += 32) l += ex2(pg[s * stride] - ref) * pg[s * stride + 1];
+        for (int s = lane; s < ns; s += 32) l += shifted(pg[s * stride + 1], pg[s * stride] - ref);
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
         if (lane == 0) s_lse[warp] = l == 0.0f ? INFINITY : log2f(l) + ref;

@@ -114,6 +114,89 @@ def test_attend_within_the_bound_of_its_arithmetic(pk, G, dtype, lens):  # noqa:
     check_close(pk, q, kind, rows, accumulate=False, scale=0.011)
 
 
+def flat_logits(n, at, z):
+    """Keys whose logit with q = 0.5 is z everywhere and 0 at the places `at`."""
+    K = np.full((n, D), z * math.sqrt(D) / (0.5 * D), np.float32)
+    K[at] = 0
+    return K
+
+
+@gpu
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("size", [1e15, 1e21, 1e28])
+def test_attend_small_weights_beside_huge_values(pk, G, size):  # noqa: F811
+    """Keys of values up to 2^96: the others' weights count all the same, in the outputs, the log-sums and acc."""
+    rng = np.random.default_rng(G)
+    n = 20001
+    V = make_rows(rng, n, torch.float32).numpy()
+    rows = []
+    for at in ([0], [n - 1], [7, 11111, n - 9]):                         # 9e-5 of a huge key's weight each, 2 in all
+        v = V.copy()
+        v[at] = size * np.sign(v[at])
+        rows.append((flat_logits(n, at, -9.3), v))
+    v = V.copy()
+    v[14000:] = np.clip(v[14000:] * np.float32(size), -7e28, 7e28)       # huge from some place on
+    rows.append((make_rows(rng, n, torch.float32).numpy(), v))
+    v = V.copy()
+    v[500] = size                                                        # nobody looks at it
+    K = make_rows(rng, n, torch.float32).numpy()
+    K[500] = -300
+    rows.append((K, v))
+    check_close(pk, torch.full((len(rows), G, D), 0.5), pk.PK_F32, rows)
+
+
+@gpu
+@pytest.mark.parametrize("G", [2, 6])
+@pytest.mark.parametrize("size", [1.0, 1e6, 1e12, 7e28])
+def test_attend_rows_of_zeros_beside_large_values(pk, G, size):  # noqa: F811
+    """Keys whose values are zero, or next to it, take their share of the weights from keys of large ones."""
+    n = 20001
+    rows = []
+    for at in ([0], [n - 1], [7, 11111, n - 9], list(range(0, n, 37))):  # 9e-5 of the others' weight each, 2 in all
+        for small in (0.0, 1e-30):
+            V = np.full((n, D), small, np.float32)
+            V[at] = size
+            rows.append((flat_logits(n, at, -9.3), V))
+    check_close(pk, torch.full((len(rows), G, D), 0.5), pk.PK_F32, rows)
+
+
+@gpu
+@pytest.mark.parametrize("G", [2, 7])
+def test_attend_values_small_then_huge(pk, G):  # noqa: F811
+    """Values far below one, then a huge one without weight, then small ones again."""
+    rng = np.random.default_rng(G)
+    n = 20001
+    K = make_rows(rng, n, torch.float32).numpy()
+    rows = []
+    for small in (1e-3, 1e-20):
+        V = make_rows(rng, n, torch.float32, small).numpy()
+        K = K.copy()
+        K[9999] = -500
+        V[9999] = 7e28
+        rows.append((K, V))
+    check_close(pk, torch.full((2, G, D), 0.5), pk.PK_F32, rows)
+
+
+@gpu
+@pytest.mark.parametrize("G", [4, 5])
+def test_attend_huge_keys(pk, G):  # noqa: F811
+    """Keys near the end of fp32's range and queries as small, of ordinary logits and of such that the largest takes all."""
+    rng = np.random.default_rng(G)
+    K, V = make_rows(rng, 300, torch.float32, 1e33).numpy(), make_rows(rng, 300, torch.float32).numpy()
+    q = make_rows(rng, G, torch.float32, 1e-33)
+    check_close(pk, q[None], pk.PK_F32, [(K, V)])
+    q = make_rows(rng, G, torch.float32, 1e-29)
+    blocks = torch.from_numpy(ref.pack(K, V)[None]).cuda()
+    c = pk.pk_quant_view(blocks, torch.full((1,), 300, dtype=torch.int32, device="cuda"), pk.PK_F32)
+    out = torch.zeros(1, G, D, device="cuda")
+    pk.pk_quant_attend(c, q.cuda()[None], G, out, torch.empty(pk.pk_quant_attend_workspace(c, G), dtype=torch.uint8, device="cuda"))
+    K, V = ref.values(blocks[0].cpu().numpy())
+    top = (q.double().numpy() @ K[:300].T).argmax(1)
+    # logits of about 1e4: the others' weights are below e^-30, together 300 e^-30, and not zero where V[top] is (head 3 of 5:
+    # e^-84 for the next one); one weight, held as a pair of halves (2^-22), times one value
+    assert np.allclose(out[0].cpu().double().numpy(), V[top], rtol=2.0 ** -20, atol=300 * math.exp(-30) * np.abs(V[:300]).max())
+
+
 # ---------------------------------------------------------------- eviction
 @gpu
 @pytest.mark.parametrize("lists", ["keep", "acc", "both", "none"])
