@@ -19,6 +19,8 @@ a token, so that the first eviction has something to go by.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import (PK_BF16, PK_F32, PK_QUANT_BLOCK_BYTES, PK_QUANT_KEYS, pk_quant_append, pk_quant_attend,
@@ -37,6 +39,8 @@ class BoundedCache:
             raise ValueError("K and V must be bf16 or fp32")
         if sink < 0 or recent < 0 or sink + recent > budget or budget < 1 or update < 1 or not 1 <= group <= 8:
             raise ValueError("need 0 <= sink, recent; sink + recent <= budget; update >= 1; 1 <= group <= 8")
+        if not 0 <= scale < math.inf:
+            raise ValueError("scale must be 0 or a finite positive number")
         self.batch, self.H, T0, self.D = K.shape
         self.G, self.budget, self.sink, self.recent, self.update = group, budget, sink, recent, update
         self.scale, self.dtype, self.device = scale, K.dtype, K.device
@@ -83,6 +87,10 @@ class BoundedCache:
             pk_quant_rows(self._cache, self.n, k, v)
         return k, v
 
+    def _check(self, name, t, shape):
+        if t.shape != shape or t.dtype != self.dtype or (t.device != self.device and not t.is_pinned()):
+            raise ValueError("%s must be %s of the cache's type, on its device or in pinned memory" % (name, list(shape)))
+
     def evict(self):
         """Drop to `budget` tokens per pair (nothing if there are no more)."""
         if self.n <= self.budget:
@@ -107,18 +115,18 @@ class BoundedCache:
         """Attend q [batch][H*G][D] over the tokens held and add the weights,
         without adding a token.  Returns the output [batch][H*G][D] fp32 (a
         buffer reused by the next call); lse holds the log-sums."""
-        if q.shape != self.out.shape or q.dtype != self.dtype:
-            raise ValueError("q must be [batch][H*G][D] of the cache's type")
+        self._check("q", q, self.out.shape)
         pk_quant_attend(self._cache, q.contiguous(), self.G, self.out, self._work, lse=self.lse, accumulate=True, scale=self.scale)
         return self.out
 
     def step(self, q, k_new, v_new):
         """One decode step: evict if the buffer is full, add the token k_new,
         v_new [batch][H][1][D], and attend q over every token held.  Everything
-        runs on torch's current stream, in order."""
-        if k_new.shape != (self.batch, self.H, 1, self.D) or v_new.shape != k_new.shape or \
-                k_new.dtype != self.dtype or v_new.dtype != self.dtype:
-            raise ValueError("k_new and v_new must be [batch][H][1][D] of the cache's type")
+        runs on torch's current stream, in order.  A step that is refused
+        changes nothing."""
+        self._check("q", q, self.out.shape)
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            self._check(name, t, (self.batch, self.H, 1, self.D))
         if self.n >= self.limit:
             self.evict()
         pk_quant_append(self._cache, k_new.contiguous(), v_new.contiguous(), 1)

@@ -238,3 +238,47 @@ def test_evict_threshold_below_zero(pk, bh, n, zeros, lists):  # noqa: F811
         assert torch.equal(a[want], b[:budget]) and b[budget:].eq(0xA5).all()          # scales
         a, b = (x[p, :, :2048].reshape(-1, 64) for x in (blocks, dst.tensors[0]))
         assert torch.equal(a[want], b[:budget]) and b[budget:].eq(0xA5).all()          # codes of K
+
+
+# ---------------------------------------------------------------- the bounded decode cache
+def bad_steps(dev, dtype):
+    """Arguments of a step of a cache of 1 x 2 pairs and 3 query heads, each with one that does not fit."""
+    q, k = torch.zeros(1, 6, D, dtype=dtype, device=dev), torch.zeros(1, 2, 1, D, dtype=dtype, device=dev)
+    other = torch.float32 if dtype == torch.bfloat16 else torch.bfloat16
+    return [(q[:, :5], k, k), (q[0], k, k), (q.to(other), k, k), (q, k[:, :1], k), (q, k.to(other), k), (q, k, k.to(other)),
+            (q, k, k[..., :64]), (q.to("meta"), k, k), (q, k.to("meta"), k), (q, k, k.to("meta"))]
+
+
+def test_bounded_cache_checks_a_step_first(pk):  # noqa: F811
+    """A step's arguments are checked before its first call (which has no GPU to run on here)."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    K = torch.zeros(1, 2, 0, D)
+    c = BoundedCache(K, K, group=3, budget=8, sink=0, recent=0)
+    for args in bad_steps("cpu", torch.float32):
+        with pytest.raises(ValueError):
+            c.step(*args)
+        assert (c.n, c.T, c.evictions) == (0, 0, 0)
+    for scale in (-1.0, math.nan, math.inf):
+        with pytest.raises(ValueError):
+            BoundedCache(K, K, group=3, budget=8, sink=0, recent=0, scale=scale)
+
+
+@gpu
+def test_bounded_cache_refused_step_changes_nothing(pk):  # noqa: F811
+    """Full or not, a refused step neither evicts nor adds; the corrected one goes on as if it had not been."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    rng = np.random.default_rng(2)
+    K, V = (make_rows(rng, 2 * 5, torch.bfloat16).view(1, 2, 5, D).cuda() for _ in range(2))
+    a, b = (BoundedCache(K, V, group=3, budget=6, sink=1, recent=2, update=2) for _ in range(2))
+    for _ in range(7):
+        q = make_rows(rng, 6, torch.bfloat16).view(1, 6, D).cuda()
+        k, v = (make_rows(rng, 2, torch.bfloat16).view(1, 2, 1, D).cuda() for _ in range(2))
+        before = [x.clone() for x in (a.positions, a.weights, *a.rows(), a._cache.tensors[1])] + [a.n, a.T, a.evictions]
+        for args in bad_steps("cuda", torch.bfloat16) + [(q.cpu(), k, v), (q, k.cpu(), v), (q, k, v.cpu())]:
+            with pytest.raises(ValueError):
+                a.step(*args)
+        after = [a.positions, a.weights, *a.rows(), a._cache.tensors[1], a.n, a.T, a.evictions]
+        assert all(torch.equal(x, y) if isinstance(x, torch.Tensor) else x == y for x, y in zip(before, after))
+        assert torch.equal(a.step(q, k, v), b.step(q, k, v))
+        assert torch.equal(a.positions, b.positions) and torch.equal(a.weights, b.weights)
+    assert a.evictions == b.evictions >= 2
