@@ -13,6 +13,10 @@ queries since they came in) is largest.  A step that finds `budget + update`
 tokens evicts down to `budget` first, into a second buffer, and the buffers
 swap; pairs choose their tokens separately.  The order of the tokens is kept.
 
+The kernels record what they find wrong on the GPU (a length out of range, rows
+that do not fit, a copy that did not arrive) in a status word; a step does not
+wait for it, check() reads it.
+
 A longer prompt comes in whole: until the first step its tokens are all there,
 and observe() lets queries of the prompt's end add their weights without adding
 a token, so that the first eviction has something to go by.
@@ -23,7 +27,7 @@ import math
 
 import torch
 
-from . import (PK_BF16, PK_F32, PK_QUANT_BLOCK_BYTES, PK_QUANT_KEYS, pk_quant_append, pk_quant_attend,
+from . import (PK_BF16, PK_F32, PK_OK, PK_QUANT_BLOCK_BYTES, PK_QUANT_KEYS, PkError, pk_quant_append, pk_quant_attend,
                pk_quant_attend_workspace, pk_quant_evict, pk_quant_rows, pk_quant_view)
 
 
@@ -51,6 +55,7 @@ class BoundedCache:
         self.n = T0                                       # tokens held per pair
         self.evictions = 0
         cap = max(T0, self.limit)
+        self._status = torch.zeros(2, dtype=torch.int32, device=self.device)     # of both buffers, whichever is in use
         self._cache, self._pos = self._buffers(cap)
         self._other = None                                # the second buffer, made at the first eviction
         self.out = torch.empty(self.batch, self.H * group, self.D, dtype=torch.float32, device=self.device)
@@ -67,7 +72,7 @@ class BoundedCache:
         cache = pk_quant_view(torch.empty(self.bh, m, PK_QUANT_BLOCK_BYTES, dtype=torch.uint8, device=dev),
                               torch.zeros(self.bh, dtype=torch.int32, device=dev), self.kind,
                               acc=torch.zeros(self.bh, m * PK_QUANT_KEYS, device=dev),
-                              status=torch.zeros(2, dtype=torch.int32, device=dev))
+                              status=self._status)
         return cache, torch.zeros(self.bh, m * PK_QUANT_KEYS, dtype=torch.int64, device=dev)
 
     @property
@@ -87,6 +92,15 @@ class BoundedCache:
             pk_quant_rows(self._cache, self.n, k, v)
         return k, v
 
+    def check(self):
+        """Wait for the calls so far on the current stream and raise PkError if
+        one of them recorded a failure on the GPU: results since the last check
+        may then be wrong.  The record is cleared."""
+        status, pair = self._status.tolist()
+        if status != PK_OK:
+            self._status.zero_()
+            raise PkError(status, "BoundedCache: pair %d" % pair)
+
     def _check(self, name, t, shape):
         if t.shape != shape or t.dtype != self.dtype or (t.device != self.device and not t.is_pinned()):
             raise ValueError("%s must be %s of the cache's type, on its device or in pinned memory" % (name, list(shape)))
@@ -105,7 +119,7 @@ class BoundedCache:
             self._other = (self._cache, self._pos)
         else:
             self._other = None
-            for t in (*self._cache.tensors, self._pos):   # the current stream may not be the one they were made on
+            for t in (*self._cache.tensors[:3], self._pos):   # the current stream may not be the one they were made on
                 t.record_stream(torch.cuda.current_stream())
         self._cache, self._pos = dst, pos
         self.n = self.budget

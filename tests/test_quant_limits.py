@@ -282,3 +282,46 @@ def test_bounded_cache_refused_step_changes_nothing(pk):  # noqa: F811
         assert torch.equal(a.step(q, k, v), b.step(q, k, v))
         assert torch.equal(a.positions, b.positions) and torch.equal(a.weights, b.weights)
     assert a.evictions == b.evictions >= 2
+
+
+def test_bounded_cache_check_reads_the_status(pk):  # noqa: F811
+    """Both buffers share one status word; check() raises what it holds, once."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    K = torch.zeros(1, 2, 0, D)
+    c = BoundedCache(K, K, group=3, budget=8, sink=0, recent=0)
+    c.check()
+    other, _ = c._buffers(8)
+    for status, pair in ((pk._lib.PK_ERR_DEVICE_CHECK, 1), (pk._lib.PK_ERR_TIMEOUT, 0)):
+        other.tensors[3].copy_(torch.tensor([status, pair], dtype=torch.int32))
+        with pytest.raises(pk.PkError) as e:
+            c.check()
+        assert e.value.status == status and "pair %d" % pair in str(e.value)
+        c.check()
+
+
+@gpu
+def test_bounded_cache_check_raises_what_the_kernels_recorded(pk):  # noqa: F811
+    """A length out of range, found before or after an eviction gave up the prompt's buffer; without one check() passes."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    rng = np.random.default_rng(3)
+    K, V = (make_rows(rng, 2 * 200, torch.float32).view(1, 2, 200, D).cuda() for _ in range(2))
+    new = [make_rows(rng, 2, torch.float32).view(1, 2, 1, D).cuda() for _ in range(2)]
+    q = make_rows(rng, 6, torch.float32).view(1, 6, D).cuda()
+    for when in ("never", "before", "after"):
+        c = BoundedCache(K, V, group=3, budget=40, sink=1, recent=20, update=8)
+        if when == "before":
+            c._cache.tensors[1][1] = -5
+            c.observe(q)
+            c._cache.tensors[1][1] = 200
+        c.step(q, *new)                  # evicts from the prompt's buffer
+        assert c.evictions == 1 and c.n == 41
+        if when == "after":
+            c._cache.tensors[1][1] = c._cache.n_cap + 1
+            c.observe(q)
+        if when == "never":
+            c.check()
+        else:
+            with pytest.raises(pk.PkError) as e:
+                c.check()
+            assert e.value.status == pk._lib.PK_ERR_DEVICE_CHECK and "pair 1" in str(e.value)
+        c.check()
