@@ -60,7 +60,7 @@ class BoundedCache:
         self._other = None                                # the second buffer, made at the first eviction
         self.out = torch.empty(self.batch, self.H * group, self.D, dtype=torch.float32, device=self.device)
         self.lse = torch.empty(self.batch, self.H * group, dtype=torch.float32, device=self.device)
-        self._work = torch.empty(pk_quant_attend_workspace(self._cache, group, True), dtype=torch.uint8, device=self.device)
+        self._work = self._workspace(self._cache)
         self._keep = torch.empty(self.bh, budget, dtype=torch.int32, device=self.device)
         if T0:
             pk_quant_append(self._cache, K.contiguous(), V.contiguous(), T0)
@@ -74,6 +74,9 @@ class BoundedCache:
                               acc=torch.zeros(self.bh, m * PK_QUANT_KEYS, device=dev),
                               status=self._status)
         return cache, torch.zeros(self.bh, m * PK_QUANT_KEYS, dtype=torch.int64, device=dev)
+
+    def _workspace(self, cache):
+        return torch.empty(pk_quant_attend_workspace(cache, self.G, True), dtype=torch.uint8, device=self.device)
 
     @property
     def positions(self):
@@ -114,12 +117,13 @@ class BoundedCache:
         dst, pos = self._other
         pk_quant_evict(self._cache, dst, self.budget, sink=self.sink, recent=self.recent, keep=self._keep)
         torch.gather(self._pos, 1, self._keep.long(), out=pos[:, :self.budget])
-        small = self._cache.n_cap == dst.n_cap            # a longer prompt's buffer is not needed again
+        small = self._cache.n_cap == dst.n_cap            # a longer prompt's buffer and workspace are not needed again
         if small:
             self._other = (self._cache, self._pos)
         else:
             self._other = None
-            for t in (*self._cache.tensors[:3], self._pos):   # the current stream may not be the one they were made on
+            work, self._work = self._work, self._workspace(dst)
+            for t in (*self._cache.tensors[:3], self._pos, work):     # the current stream may not be the one they were made on
                 t.record_stream(torch.cuda.current_stream())
         self._cache, self._pos = dst, pos
         self.n = self.budget

@@ -325,3 +325,26 @@ def test_bounded_cache_check_raises_what_the_kernels_recorded(pk):  # noqa: F811
                 c.check()
             assert e.value.status == pk._lib.PK_ERR_DEVICE_CHECK and "pair 1" in str(e.value)
         c.check()
+
+
+@gpu
+def test_bounded_cache_gives_up_a_long_prompt(pk):  # noqa: F811
+    """After the eviction of a long prompt the cache holds what its bound needs: blocks, positions and workspace."""
+    from kv_cache_top_b200.bounded_cache import BoundedCache
+    T0 = 30000
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    K = torch.zeros(1, 2, T0, D, dtype=torch.bfloat16, device="cuda")
+    c = BoundedCache(K, K, group=4, budget=64, sink=1, recent=20, update=64)
+    q, k = torch.zeros(1, 8, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, 1, D, dtype=torch.bfloat16, device="cuda")
+    del K
+    for _ in range(130):                 # past the second eviction
+        c.step(q, k, k)
+    c.check()
+    assert c.evictions == 3
+    small = pk.pk_quant_attend_workspace(c._cache, 4, True)
+    assert c._work.numel() == small
+    # two buffers of 128 keys (144 bytes, a weight, a position), outputs, the list, the arguments; torch rounds up to 512
+    room = small + 2 * 2 * 128 * (144 + 4 + 8) + 32 * 1024
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before <= room < T0 * 2 * 144
