@@ -240,6 +240,33 @@ def test_evict_threshold_below_zero(pk, bh, n, zeros, lists):  # noqa: F811
         assert torch.equal(a[want], b[:budget]) and b[budget:].eq(0xA5).all()          # codes of K
 
 
+@gpu
+@pytest.mark.parametrize("cap", [1024, 40032, 131104])
+@pytest.mark.parametrize("budget,sink,recent", [(500, 5, 10), (30, 10, 20), (900, 0, 900), (1000, 1000, 0)])
+def test_evict_of_bad_and_short_lengths(pk, cap, budget, sink, recent):  # noqa: F811
+    """Lengths beyond the room or below zero are read as the bounds and recorded; pairs within the budget keep all; a
+    budget that sink and recent use up; all in one call, whatever kernel the room asks for."""
+    lens = [cap, 0, 1, budget, budget + 1, cap + 7, -3]
+    use = [min(max(n, 0), cap) for n in lens]
+    g = torch.Generator(device="cuda").manual_seed(cap + budget)
+    blocks = torch.randint(0, 256, (len(lens), cap // KEYS, BLOCK), generator=g, device="cuda", dtype=torch.uint8)
+    acc = torch.rand(len(lens), cap, generator=g, device="cuda")
+    src = pk.pk_quant_view(blocks, torch.tensor(lens, dtype=torch.int32, device="cuda"), pk.PK_BF16, acc=acc,
+                           status=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    dst = pk.pk_quant_view(torch.zeros(len(lens), 32, BLOCK, dtype=torch.uint8, device="cuda"),
+                           torch.zeros(len(lens), dtype=torch.int32, device="cuda"), pk.PK_BF16)
+    keep = torch.zeros(len(lens), budget, dtype=torch.int32, device="cuda")
+    pk.pk_quant_evict(src, dst, budget, sink=sink, recent=recent, keep=keep)
+    assert src.tensors[3][0].item() == pk._lib.PK_ERR_DEVICE_CHECK and src.tensors[3][1].item() in (5, 6)
+    for p, n in enumerate(use):
+        want = ref.evict(acc[p].cpu().numpy(), n, budget, sink, recent)
+        assert dst.tensors[1][p].item() == len(want)
+        assert keep[p].tolist() == want.tolist() + [-1] * (budget - len(want))
+        rows = torch.from_numpy(want).cuda()
+        a, b = (x[p, :, :2048].reshape(-1, 64) for x in (blocks, dst.tensors[0]))
+        assert torch.equal(a[rows], b[:len(want)]) and b[len(want):].eq(0).all()
+
+
 # ---------------------------------------------------------------- the bounded decode cache
 def bad_steps(dev, dtype):
     """Arguments of a step of a cache of 1 x 2 pairs and 3 query heads, each with one that does not fit."""
