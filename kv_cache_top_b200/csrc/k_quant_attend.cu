@@ -350,7 +350,6 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
     };
     int slot = 0;
     uint32_t parity = 0;
-    int late = -1;                       // pair of a block that did not arrive
     const int head = WIDE ? g : (g & 3);
     const float low = !WIDE && g >= 4 ? -1.0f : 0.0f;   // this column holds the weights' low parts
 
@@ -415,7 +414,7 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
 #pragma unroll 1
             for (; x < stop; x += SPAN) {
                 uint8_t *blk = sm.ring[warp][slot];
-                if (!wait_block(&sm.bar[warp][slot], parity)) late = p;
+                if (!wait_block(&sm.bar[warp][slot], parity) && lane == 0) quant_late(a.c.status, p);
                 const int b = (int)(x - first), valid = min(kQKeys, n - b * kQKeys);
                 {   // scales as fp32 (zero behind the length), two groups of two keys a lane
                     const int pair = lane >> 1, half = lane & 1;
@@ -617,7 +616,6 @@ __device__ __forceinline__ void attend_blocks(const QuantAttendArgs &a, QaSmem &
         first += nb;
         p = next;
     }
-    if (late >= 0 && lane == 0 && a.c.status && atomicCAS(a.c.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.c.status[1] = late;
 }
 
 // A worker is a CTA, or 4 warps of one.  Large workers leave fewer partial

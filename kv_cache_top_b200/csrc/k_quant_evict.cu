@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kQeThreads, 2) k_quant_evict(QuantEvictArgs a)
         move_rows(a, p, lane < m ? (int)sm.list[j + lane] : 0, m, j, true);
     }
     finish(a, p, n, kQeThreads);
-    if (late && tid == 0 && a.src.status && atomicCAS(a.src.status, 0, (int)PK_ERR_TIMEOUT) == 0) a.src.status[1] = p;
+    if (late && tid == 0) quant_late(a.src.status, p);
 }
 
 // where a long pair's kept slots are listed: null where the select kernel moves the rows

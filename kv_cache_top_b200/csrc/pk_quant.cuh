@@ -32,6 +32,11 @@ __device__ __forceinline__ void quant_devchk(int32_t *status, int p)
 {
     if (status && atomicCAS(status, 0, (int)PK_ERR_DEVICE_CHECK) == 0) status[1] = p;
 }
+// ... or that a bounded wait for one of its copies gave up.
+__device__ __forceinline__ void quant_late(int32_t *status, int p)
+{
+    if (status && atomicCAS(status, 0, (int)PK_ERR_TIMEOUT) == 0) status[1] = p;
+}
 
 // Length of pair p within [0, n_cap].
 __device__ __forceinline__ int quant_len(const QuantCache &c, int p)
