@@ -6,10 +6,11 @@
 // kernel, which knows each head's log-sum, adds the weights to acc.
 //
 // 144 bytes a key of HBM are the floor (64 pairs of 131072 keys, 4 heads: 184
-// us; the kernel takes 266, at a 1770 MHz power cap 300).  What bounds it is
-// the instructions that make matrix operands of codes and sums of digits: 717
-// warp instructions a block of 32 keys, issue slots 65% full, the integer pipe
-// 52%, fp32 44%, matrix 23%.  Hence bytes and not halves for the logits (292
+// us; the kernel takes 267, at the power cap 298 to 306; 8 heads 357).  What
+// bounds it is the instructions that make matrix operands of codes and sums of
+// digits: 751 warp instructions a block of 32 keys, issue slots 67% full, the
+// integer pipe 52%, fp32 46%, matrix 23% (8 heads: 869, 60%, 39%, 43%, 35%).
+// Hence bytes and not halves for the logits (292
 // us to 275), two fp32 operations an instruction (291 to 276), and 16 warps
 // with two blocks each in flight and not 8 or 12 with more (320 and 296).
 // Calls of few keys are bound by latency: two launches, a plan, one round of
