@@ -114,6 +114,28 @@ def test_attend_within_the_bound_of_its_arithmetic(pk, G, dtype, lens):  # noqa:
     check_close(pk, q, kind, rows, accumulate=False, scale=0.011)
 
 
+@gpu
+@pytest.mark.parametrize("G", [3, 4, 5, 8])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_attend_poisoned_query_head(pk, G, bad):  # noqa: F811
+    """A NaN or an infinity in one head's query makes that head NaN, of every pair length, and no other."""
+    rng = np.random.default_rng(G)
+    lens = [1, 32, 33, 700]
+    c, blocks = make_cache(pk, rng, lens, 704, pk.PK_F32)
+    q = torch.stack([make_rows(rng, G, torch.float32) for _ in lens])
+    for p in range(len(lens)):
+        q[p, p % G, 37 * p % D] = bad
+    out, lse = torch.zeros(len(lens), G, D, device="cuda"), torch.zeros(len(lens), G, device="cuda")
+    pk.pk_quant_attend(c, q.cuda(), G, out, torch.empty(pk.pk_quant_attend_workspace(c, G), dtype=torch.uint8, device="cuda"), lse=lse)
+    out, lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    for p, n in enumerate(lens):
+        K, V = (x[:n] for x in ref.values(blocks[p]))
+        ok = [g for g in range(G) if g != p % G]
+        assert np.isnan(out[p, p % G]).all() and np.isnan(lse[p, p % G])
+        o, l, _, eo, el, _ = bound.attend(q[p, ok].double().numpy(), K, V)
+        assert np.all(np.abs(out[p, ok] - o) <= eo) and np.all(np.abs(lse[p, ok] - l) <= el)
+
+
 def flat_logits(n, at, z):
     """Keys whose logit with q = 0.5 is z everywhere and 0 at the places `at`."""
     K = np.full((n, D), z * math.sqrt(D) / (0.5 * D), np.float32)
